@@ -35,6 +35,7 @@ IMQ_DIR_NONE, IMQ_DIR_OUTER, IMQ_DIR_INNER, IMQ_DIR_BOTH = 0, 1, 2, 3
 IMQ_MAX_GROUPS = 64
 IMQ_NOALLOC_SCRATCH_BYTES = 8 << 20
 IMQ_RTN_CLIP = 1
+IMQ_W4_BLOCK = 128
 
 _TORCH_TO_IMQ = {torch.float32: IMQ_F32, torch.bfloat16: IMQ_BF16, torch.int16: IMQ_I16,
                  torch.int32: IMQ_I32, torch.int64: IMQ_I64}
@@ -73,6 +74,13 @@ class imq_group(ctypes.Structure):
                 ("k_len", ctypes.c_int64), ("k_len_padded", ctypes.c_int64)]
 
 
+class imq_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("steps", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int64), ("k_page_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64),
+                ("steps_page_stride", ctypes.c_int64), ("page_size", ctypes.c_int32), ("n_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("bits", ctypes.c_int32)]
+
+
 # Names and argument types of every entry point of include/imq.h.
 _VP, _I32, _I64, _F64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_double, ctypes.c_size_t
 SIGNATURES = {
@@ -104,6 +112,14 @@ SIGNATURES = {
                                   _I64, _I64, _VP],
     "imq_unpacked_gemm_batched": [_I32, _VP, _VP, _I64, _VP, _I64, _VP, _I64, _I32, _VP, _I64, _I32, _VP, _I64, _I32,
                                   _I64, _VP, _I64, _I64, _VP, _SZ, _VP],
+    "imq_w4_quantize": [_VP, _I32, _I64, _I64, _I64, _I32, _I32, _VP, _I64, _VP, _I64, _VP],
+    "imq_w4_dequantize": [_VP, _I64, _VP, _I64, _I64, _I64, _I32, _VP, _I32, _I64, _I32, _VP],
+    "imq_w4_matvec": [_VP, _I64, _VP, _I64, _I64, _I64, _I32, _VP, _I32, _I64, _I64, _VP, _I32, _I64, _VP],
+    "imq_kv_write": [_VP, _VP, _I64, _I64, _VP, _I64, _I64, _I32, _I64, _VP, _VP],
+    "imq_kv_read": [_VP, _VP, _I64, _VP, _I64, _I64, _VP, _I64, _I64, _I32, _VP],
+    "imq_paged_attention_workspace": [_VP, _I64, _I32, _I64, _VP],
+    "imq_paged_attention": [_VP, _VP, _I32, _I64, _I64, _I64, _I32, _VP, _I64, _I64, _VP, _I64, ctypes.c_float, _VP, _I32,
+                            _I64, _I64, _VP, _I64, _VP, _SZ, _VP],
     "imq_device_status": [_VP, _I32],
     "imq_check_bounded_wait": [ctypes.c_uint64, _VP],
     "imq_status_str": [_I32],
@@ -539,3 +555,234 @@ def imq_gemm_unpacked_batched(batch: PlanBatch, workspace: torch.Tensor, deltaA,
                                          _TORCH_TO_IMQ[C.dtype] if C is not None else IMQ_I32, ldc, _ptr(Cf), strideCf,
                                          ldcf, _stream(stream))
     _check(st, "imq_gemm_unpacked_batched")
+
+
+# ------------------------------------------------------------------------------------------------
+# 5. one decoding step: 4-bit weights, a low-bit cache, attention over it
+# ------------------------------------------------------------------------------------------------
+_FLOAT_TO_IMQ = {torch.float32: IMQ_F32, torch.bfloat16: IMQ_BF16}
+
+
+def _float_dtype(dtype, what: str) -> int:
+    t = _FLOAT_TO_IMQ.get(dtype)
+    if t is None:
+        raise ValueError(f"{what} must be float32 or bfloat16, not {dtype}")
+    return t
+
+
+def _on_device(*tensors):
+    """The calls launch on the current device: every tensor has to be there."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != dev):
+            raise ValueError(f"expected a tensor on the current CUDA device, got one on {t.device}")
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor of the stream that will use it (so that its memory is not handed on too early)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(s):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+class W4Weight:
+    """A weight in 4 bits (K inputs, N output channels, a step per `group` inputs): `codes` (N, bytes of a row)
+    uint8 and `steps` (N, groups) float32 in the storage of include/imq.h, both with unit column stride."""
+
+    def __init__(self, codes: torch.Tensor, steps: torch.Tensor, K: int, N: int, group: int):
+        K, N, group = int(K), int(N), int(group)
+        if group not in (32, 64, 128):
+            raise ValueError(f"group must be 32, 64 or 128, not {group}")
+        if codes.dtype != torch.uint8 or codes.dim() != 2 or steps.dtype != torch.float32 or steps.dim() != 2:
+            raise ValueError("codes must be a uint8 and steps a float32 matrix")
+        if codes.size(0) != N or steps.size(0) != N or codes.size(1) < self.row_bytes(K) or steps.size(1) < -(-K // group):
+            raise ValueError(f"codes {tuple(codes.shape)} and steps {tuple(steps.shape)} do not hold {K} x {N} in groups of {group}")
+        if codes.device != steps.device:
+            raise ValueError("codes and steps must be on one device")
+        self.codes, self.steps, self.K, self.N, self.group = codes, steps, K, N, group
+        ldc, lds = (_ld(t) if t.numel() else t.size(1) for t in (codes, steps))
+        self._args = (codes.data_ptr(), ldc, steps.data_ptr(), lds, K, N, group)
+
+    @staticmethod
+    def row_bytes(K: int) -> int:
+        return -(-K // IMQ_W4_BLOCK) * (IMQ_W4_BLOCK // 2)
+
+
+def imq_w4_quantize(W: torch.Tensor, group: int = 128, transW: bool = False, codes=None, steps=None,
+                    stream=None) -> W4Weight:
+    """A float32 or bfloat16 weight, stored K x N (N x K when transW), in 4 bits."""
+    wt = _float_dtype(W.dtype, "W")
+    _on_device(W, codes, steps)
+    ld = _ld(W)
+    N, K = W.shape if transW else (W.shape[1], W.shape[0])
+    if codes is None:
+        codes = _empty((N, W4Weight.row_bytes(K)), torch.uint8, W.device, stream)
+    if steps is None:
+        steps = _empty((N, -(-K // int(group)) if int(group) > 0 else 0), torch.float32, W.device, stream)
+    w = W4Weight(codes, steps, K, N, group)
+    _check(lib().imq_w4_quantize(W.data_ptr(), wt, K, N, ld, int(transW), w.group, *w._args[:4], _stream(stream)),
+           "imq_w4_quantize")
+    return w
+
+
+def imq_w4_dequantize(weight: W4Weight, dtype=torch.float32, transW: bool = False, out=None, stream=None) -> torch.Tensor:
+    """The values of a 4-bit weight, K x N (N x K when transW)."""
+    shape = (weight.N, weight.K) if transW else (weight.K, weight.N)
+    if out is None:
+        out = _empty(shape, dtype, weight.codes.device, stream)
+    elif tuple(out.shape) != shape:
+        raise ValueError(f"out must be {shape}")
+    wt = _float_dtype(out.dtype, "out")
+    _on_device(weight.codes, out)
+    _check(lib().imq_w4_dequantize(*weight._args, out.data_ptr(), wt, _ld(out), int(transW), _stream(stream)),
+           "imq_w4_dequantize")
+    return out
+
+
+def imq_w4_matvec(weight: W4Weight, X: torch.Tensor, out=None, out_dtype=None, stream=None) -> torch.Tensor:
+    """X (M x K) times a 4-bit weight: M x N in out's dtype, out_dtype, or X's."""
+    xt = _float_dtype(X.dtype, "X")
+    if X.dim() != 2 or X.size(1) != weight.K:
+        raise ValueError(f"X must be M x {weight.K}, not {tuple(X.shape)}")
+    M = X.size(0)
+    if out is None:
+        out = _empty((M, weight.N), X.dtype if out_dtype is None else out_dtype, X.device, stream)
+    elif tuple(out.shape) != (M, weight.N) or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError(f"out must be {M} x {weight.N} of the output's dtype")
+    _on_device(weight.codes, X, out)
+    _check(lib().imq_w4_matvec(*weight._args, X.data_ptr(), xt, M, _ld(X), out.data_ptr(), _float_dtype(out.dtype, "out"),
+                               _ld(out), _stream(stream)), "imq_w4_matvec")
+    return out
+
+
+class KVCache:
+    """A paged cache of keys and values in `bits` (8 or 4) bits: `k` and `v` (pages, heads, page size, bytes of a
+    vector) uint8, `steps` (pages, heads, page size, 2) float32, contiguous within a page.  A slot is
+    page * page_size + position."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, steps: torch.Tensor, head_dim: int, bits: int):
+        head_dim, bits = int(head_dim), int(bits)
+        if bits not in (4, 8):
+            raise ValueError(f"bits must be 4 or 8, not {bits}")
+        if k.dim() != 4 or k.dtype != torch.uint8 or v.dtype != torch.uint8 or k.shape != v.shape:
+            raise ValueError("k and v must be equal-shaped uint8 tensors (pages, heads, page size, bytes of a vector)")
+        if k.size(3) * 8 != head_dim * bits:
+            raise ValueError(f"a vector of {head_dim} codes takes {head_dim * bits / 8:g} bytes, not {k.size(3)}")
+        if steps.dtype != torch.float32 or tuple(steps.shape) != (*k.shape[:3], 2):
+            raise ValueError("steps must be float32 (pages, heads, page size, 2)")
+        if k.device != v.device or k.device != steps.device:
+            raise ValueError("k, v and steps must be on one device")
+        pages, heads, page_size, _ = k.shape
+        strides = []
+        for t in (k, v, steps):
+            per_page = t.size(1) * t.size(2) * t.size(3)
+            if pages and not t[0].is_contiguous():
+                raise ValueError("a page must be contiguous")
+            strides.append(t.stride(0) if pages > 1 else -(-per_page // 16) * 16)
+        self.k, self.v, self.steps = k, v, steps
+        self.n_pages, self.page_size, self.n_heads, self.head_dim, self.bits = pages, page_size, heads, head_dim, bits
+        self.raw = imq_kv_cache(k.data_ptr(), v.data_ptr(), steps.data_ptr(), pages, *strides, page_size, heads, head_dim, bits)
+        self._ref = ctypes.addressof(self.raw)
+        self._workspace = {}  # (batch, query heads, max_len) -> bytes
+
+    @classmethod
+    def zeros(cls, n_pages: int, page_size: int, n_heads: int, head_dim: int, bits: int = 8, device="cuda") -> "KVCache":
+        k = torch.zeros((n_pages, n_heads, page_size, head_dim * bits // 8), dtype=torch.uint8, device=device)
+        return cls(k, torch.zeros_like(k), torch.zeros((n_pages, n_heads, page_size, 2), device=device), head_dim, bits)
+
+
+def _vectors(t, cache: KVCache, n: int, what: str):
+    """(pointer, token stride, head stride) of (n, heads, head_dim) vectors."""
+    if tuple(t.shape) != (n, cache.n_heads, cache.head_dim) or t.stride(2) != 1:
+        raise ValueError(f"{what} must be ({n}, {cache.n_heads}, {cache.head_dim}) with unit stride in the last axis")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _slots(slots) -> int:
+    if slots.dtype != torch.int64 or slots.dim() != 1 or (slots.numel() > 1 and slots.stride(0) != 1):
+        raise ValueError("slots must be a contiguous int64 vector")
+    return slots.numel()
+
+
+def imq_kv_write(cache: KVCache, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, stream=None):
+    """Quantises the tokens' keys and values (n, heads, head_dim) into their slots; negative slots are skipped."""
+    xt = _float_dtype(K.dtype, "K")
+    if V.dtype != K.dtype:
+        raise ValueError("K and V must have one dtype")
+    n = _slots(slots)
+    _on_device(cache.k, K, V, slots)
+    _check(lib().imq_kv_write(cache._ref, *_vectors(K, cache, n, "K"), *_vectors(V, cache, n, "V"), xt, n, slots.data_ptr(),
+                              _stream(stream)), "imq_kv_write")
+
+
+def imq_kv_read(cache: KVCache, slots: torch.Tensor, dtype=torch.float32, K=None, V=None, stream=None):
+    """(K, V) of the slots, each (n, heads, head_dim).  Rows of negative slots are left as they were: not
+    initialised where this call allocates the output."""
+    n = _slots(slots)
+    shape = (n, cache.n_heads, cache.head_dim)
+    if K is None:
+        K = _empty(shape, dtype if V is None else V.dtype, cache.k.device, stream)
+    if V is None:
+        V = _empty(shape, K.dtype, cache.k.device, stream)
+    yt = _float_dtype(K.dtype, "K")
+    if V.dtype != K.dtype:
+        raise ValueError("K and V must have one dtype")
+    _on_device(cache.k, slots, K, V)
+    _check(lib().imq_kv_read(cache._ref, slots.data_ptr(), n, *_vectors(K, cache, n, "K"), *_vectors(V, cache, n, "V"), yt,
+                             _stream(stream)), "imq_kv_read")
+    return K, V
+
+
+def imq_paged_attention_workspace(cache: KVCache, batch: int, n_q_heads: int, max_len: int) -> int:
+    """Workspace bytes of imq_paged_attention for these sizes."""
+    key = (batch, n_q_heads, max_len)
+    if key not in cache._workspace:
+        if len(cache._workspace) >= 64:  # lengths that grow step by step
+            cache._workspace.clear()
+        n = ctypes.c_size_t(0)
+        _check(lib().imq_paged_attention_workspace(cache._ref, *key, ctypes.addressof(n)), "imq_paged_attention_workspace")
+        cache._workspace[key] = n.value
+    return cache._workspace[key]
+
+
+def imq_paged_attention(cache: KVCache, Q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, max_len=None,
+                        scale=None, out=None, out_dtype=None, lse=None, want_lse=True, workspace=None, stream=None):
+    """Attention of one token per sequence, Q (batch, query heads, head_dim), over the sequences' cached tokens:
+    (out, lse), lse None unless wanted.  block_table int32 (batch, pages of the longest), seq_lens int32 (batch).
+    max_len bounds seq_lens (default: what the table covers); scale defaults to head_dim ** -0.5."""
+    qt = _float_dtype(Q.dtype, "Q")
+    if Q.dim() != 3 or Q.size(2) != cache.head_dim or Q.stride(2) != 1:
+        raise ValueError(f"Q must be (batch, query heads, {cache.head_dim}) with unit stride in the last axis")
+    batch, heads, _ = Q.shape
+    if heads == 0 or heads % cache.n_heads:
+        raise ValueError(f"{heads} query heads on {cache.n_heads} key heads")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.size(0) != batch or (
+            block_table.size(1) > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be int32 (batch, pages) with unit stride in the last axis")
+    if seq_lens.dtype != torch.int32 or tuple(seq_lens.shape) != (batch,) or (batch > 1 and seq_lens.stride(0) != 1):
+        raise ValueError("seq_lens must be a contiguous int32 vector of the batch")
+    width = block_table.size(1)
+    max_len = width * cache.page_size if max_len is None else int(max_len)
+    if out is None:
+        out = _empty((batch, heads, cache.head_dim), Q.dtype if out_dtype is None else out_dtype, Q.device, stream)
+    elif out.shape != Q.shape or out.stride(2) != 1 or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError("out must have Q's shape, unit stride in the last axis and the output's dtype")
+    ot = _float_dtype(out.dtype, "out")
+    if lse is None:
+        if want_lse:
+            lse = _empty((batch, heads), torch.float32, Q.device, stream)
+    elif lse.dtype != torch.float32 or tuple(lse.shape) != (batch, heads) or (heads > 1 and lse.stride(1) != 1):
+        raise ValueError("lse must be float32 (batch, query heads) with unit stride in the last axis")
+    need = imq_paged_attention_workspace(cache, batch, heads, max_len)
+    if workspace is None and need:
+        workspace = _empty(need, torch.uint8, Q.device, stream)
+    _on_device(cache.k, Q, block_table, seq_lens, out, lse, workspace)
+    _check(lib().imq_paged_attention(
+        cache._ref, Q.data_ptr(), qt, Q.stride(0), Q.stride(1), batch, heads, block_table.data_ptr(), block_table.stride(0),
+        width, seq_lens.data_ptr(), max_len, cache.head_dim ** -0.5 if scale is None else float(scale), out.data_ptr(), ot,
+        out.stride(0), out.stride(1), None if lse is None else lse.data_ptr(), 0 if lse is None else lse.stride(0),
+        None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)), "imq_paged_attention")
+    return out, lse

@@ -22,8 +22,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libimq.so")
 LIB_DEBUG = os.path.join(PKG, "libimq_debug.so")
-SOURCES = ["api.cu", "rtn.cu", "plan.cu", "unpack.cu", "gemm.cu"]
-HEADERS = ["common.cuh", "internal.h"]
+SOURCES = ["api.cu", "rtn.cu", "plan.cu", "unpack.cu", "gemm.cu", "w4.cu", "kv.cu", "attn.cu"]
+HEADERS = ["common.cuh", "internal.h", "lowbit.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

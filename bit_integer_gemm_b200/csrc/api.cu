@@ -524,6 +524,55 @@ imq_status imq_unpacked_gemm_batched(int32_t batch, imq_plan_t* const* plans, co
                                    gB, Cint, strideC, ct, ldc, Cf, strideCf, ldcf, stream);
 }
 
+imq_status imq_w4_quantize(const void* W, imq_dtype wt, int64_t K, int64_t N, int64_t ldw, int32_t transW, int32_t group,
+                           uint8_t* codes, int64_t ldc, float* steps, int64_t lds, imq_stream_t stream) {
+  return imq::launch_w4_quantize(W, wt, K, N, ldw, transW, group, codes, ldc, steps, lds,
+                                 reinterpret_cast<cudaStream_t>(stream));
+}
+
+imq_status imq_w4_dequantize(const uint8_t* codes, int64_t ldc, const float* steps, int64_t lds, int64_t K, int64_t N,
+                             int32_t group, void* W, imq_dtype wt, int64_t ldw, int32_t transW, imq_stream_t stream) {
+  return imq::launch_w4_dequantize(codes, ldc, steps, lds, K, N, group, W, wt, ldw, transW,
+                                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+imq_status imq_w4_matvec(const uint8_t* codes, int64_t ldc, const float* steps, int64_t lds, int64_t K, int64_t N,
+                         int32_t group, const void* X, imq_dtype xt, int64_t M, int64_t ldx, void* Y, imq_dtype yt,
+                         int64_t ldy, imq_stream_t stream) {
+  return imq::launch_w4_matvec(codes, ldc, steps, lds, K, N, group, X, xt, M, ldx, Y, yt, ldy,
+                               reinterpret_cast<cudaStream_t>(stream));
+}
+
+imq_status imq_kv_write(const imq_kv_cache* cache, const void* K, int64_t k_token_stride, int64_t k_head_stride,
+                        const void* V, int64_t v_token_stride, int64_t v_head_stride, imq_dtype xt, int64_t n,
+                        const int64_t* slots, imq_stream_t stream) {
+  return imq::launch_kv_write(cache, K, k_token_stride, k_head_stride, V, v_token_stride, v_head_stride, xt, n, slots,
+                              reinterpret_cast<cudaStream_t>(stream));
+}
+
+imq_status imq_kv_read(const imq_kv_cache* cache, const int64_t* slots, int64_t n, void* K, int64_t k_token_stride,
+                       int64_t k_head_stride, void* V, int64_t v_token_stride, int64_t v_head_stride, imq_dtype yt,
+                       imq_stream_t stream) {
+  return imq::launch_kv_read(cache, slots, n, K, k_token_stride, k_head_stride, V, v_token_stride, v_head_stride, yt,
+                             reinterpret_cast<cudaStream_t>(stream));
+}
+
+imq_status imq_paged_attention_workspace(const imq_kv_cache* cache, int64_t batch, int32_t n_q_heads, int64_t max_len,
+                                         size_t* bytes) {
+  return imq::paged_attention_workspace(cache, batch, n_q_heads, max_len, bytes);
+}
+
+imq_status imq_paged_attention(const imq_kv_cache* cache, const void* Q, imq_dtype qt, int64_t q_batch_stride,
+                               int64_t q_head_stride, int64_t batch, int32_t n_q_heads, const int32_t* block_table,
+                               int64_t table_stride, int64_t table_width, const int32_t* seq_lens, int64_t max_len,
+                               float scale, void* out, imq_dtype ot, int64_t o_batch_stride, int64_t o_head_stride,
+                               float* lse, int64_t lse_batch_stride, void* workspace, size_t workspace_bytes,
+                               imq_stream_t stream) {
+  return imq::launch_paged_attention(cache, Q, qt, q_batch_stride, q_head_stride, batch, n_q_heads, block_table, table_stride,
+                                     table_width, seq_lens, max_len, scale, out, ot, o_batch_stride, o_head_stride, lse,
+                                     lse_batch_stride, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
 imq_status imq_check_bounded_wait(uint64_t timeout_ns, imq_stream_t stream) {
   if (timeout_ns < 1000ull || timeout_ns > 1000000000ull) return IMQ_ERR_ARG;
   DeviceState* ds;

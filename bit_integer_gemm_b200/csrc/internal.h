@@ -156,6 +156,28 @@ struct GemmSpec {
 bool b_group_positions(const imq_plan_t* pl, std::vector<float>* pos);
 // The GEMMs of n problems in as few launches as the problem table allows (gemm.cu).
 imq_status launch_gemm_multi(const GemmSpec* specs, int n, cudaStream_t stream);
+
+// 4-bit weights (w4.cu): imq_w4_*.
+imq_status launch_w4_quantize(const void* W, imq_dtype wt, int64_t K, int64_t N, int64_t ldw, int32_t transW, int32_t group,
+                              uint8_t* codes, int64_t ldc, float* steps, int64_t lds, cudaStream_t st);
+imq_status launch_w4_dequantize(const uint8_t* codes, int64_t ldc, const float* steps, int64_t lds, int64_t K, int64_t N,
+                                int32_t group, void* W, imq_dtype wt, int64_t ldw, int32_t transW, cudaStream_t st);
+imq_status launch_w4_matvec(const uint8_t* codes, int64_t ldc, const float* steps, int64_t lds, int64_t K, int64_t N,
+                            int32_t group, const void* X, imq_dtype xt, int64_t M, int64_t ldx, void* Y, imq_dtype yt,
+                            int64_t ldy, cudaStream_t st);
+// The paged cache (kv.cu): imq_kv_*; check_cache is what every call on a cache checks first.
+imq_status check_cache(const imq_kv_cache* cache);
+imq_status launch_kv_write(const imq_kv_cache* c, const void* K, int64_t k_tok, int64_t k_head, const void* V, int64_t v_tok,
+                           int64_t v_head, imq_dtype t, int64_t n, const int64_t* slots, cudaStream_t st);
+imq_status launch_kv_read(const imq_kv_cache* c, const int64_t* slots, int64_t n, void* K, int64_t k_tok, int64_t k_head,
+                          void* V, int64_t v_tok, int64_t v_head, imq_dtype t, cudaStream_t st);
+// Attention over the paged cache (attn.cu).
+imq_status paged_attention_workspace(const imq_kv_cache* c, int64_t batch, int32_t q_heads, int64_t max_len, size_t* bytes);
+imq_status launch_paged_attention(const imq_kv_cache* c, const void* Q, imq_dtype qt, int64_t q_batch, int64_t q_head,
+                                  int64_t batch, int32_t q_heads, const int32_t* table, int64_t table_stride,
+                                  int64_t table_width, const int32_t* lens, int64_t max_len, float scale, void* out,
+                                  imq_dtype ot, int64_t o_batch, int64_t o_head, float* lse, int64_t lse_batch,
+                                  void* workspace, size_t workspace_bytes, cudaStream_t st);
 }  // namespace imq
 
 #define IMQ_CUDA_TRY(expr)                                    \

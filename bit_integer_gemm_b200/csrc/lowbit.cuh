@@ -1,0 +1,165 @@
+// lowbit.cuh -- device helpers of the low-bit weight and cache kernels (w4.cu, kv.cu, attn.cu): the
+// quantisation rule of a group, the storage of 4-bit codes, their way into the tensor cores' operands.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace imq {
+
+// ------------------------------------------------------------------------------------------------
+// quantisation of one group: imq_rtn_quantize's rule with p = 1 (q = max |x|)
+// ------------------------------------------------------------------------------------------------
+// The bits of |x| order like unsigned integers, infinities and NaNs above every finite value, so one
+// integer maximum finds q and any non-finite entry.
+__device__ __forceinline__ uint32_t abs_key(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+__device__ __forceinline__ bool key_finite(uint32_t key) { return key < 0x7F800000u; }
+
+// s = beta / q and the step q / beta, correctly rounded.  A group of zeros, or one so small that s would
+// leave fp32, takes s = step = 1 (its codes are 0); a non-finite group's step is NaN.
+__device__ __forceinline__ void group_scale(uint32_t key, float beta, float* s, float* step) {
+  const float q = __uint_as_float(key);
+  if (!key_finite(key)) {
+    *s = 0.f;
+    *step = __uint_as_float(0x7FC00000u);
+    return;
+  }
+  *s = __fdiv_rn(beta, q);
+  *step = __fdiv_rn(q, beta);
+  if (q == 0.f || !key_finite(__float_as_uint(*s))) *s = *step = 1.f;
+}
+
+// round_half_even(fp32(x * s)) + bias for |x * s| <= 128: adding 1.5 * 2^23 rounds to an integer in the low
+// mantissa bits.  (|x| <= q, so |fp32(x * s)| is at most beta but for the rounding of s, well below beta + 1/2.)
+// s = 0 marks a non-finite group, whose codes are 0 whatever x is.
+__device__ __forceinline__ uint32_t code_of(float x, float s, uint32_t bias) {
+  if (s == 0.f) return bias;
+  return (__float_as_uint(__fadd_rn(__fmul_rn(x, s), 12582912.f)) + bias) & 0xFFu;
+}
+
+// Eight 4-bit codes in a word: code e in bits 4 * (e / 2 + 4 * (e % 2)), so that one mask leaves the codes
+// 2i and 2i + 1 in the two halves of a register.
+__device__ __forceinline__ uint32_t pack_nibbles(const uint32_t (&u)[8]) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w |= u[e] << (4 * (e / 2 + 4 * (e % 2)));
+  return w;
+}
+__device__ __forceinline__ float nibble_value(uint32_t w, int e) {
+  return (float)(int32_t)((w >> (4 * (e / 2 + 4 * (e % 2)))) & 15u) - 8.f;
+}
+
+// ------------------------------------------------------------------------------------------------
+// element types
+// ------------------------------------------------------------------------------------------------
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) {
+  return x;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+
+// Eight consecutive entries, 16-byte aligned.
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 v = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]),
+                                            bf16_pair(x[6], x[7]));
+}
+
+// ------------------------------------------------------------------------------------------------
+// warp-level tensor-core products, fp32 sums: D (16 x 8) += A (16 x 16) * B (16 x 8).  With g = lane / 4
+// and c = lane % 4: a0, a2 are row g at inner positions 2c, 2c+1 and 2c+8, 2c+9; a1, a3 row g + 8; b0, b1
+// column g at the same positions; d0, d1 row g and d2, d3 row g + 8 at columns 2c, 2c+1.
+// ------------------------------------------------------------------------------------------------
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Codes as fp16 or bf16 pairs without integer-to-float conversions: a code's bits are set into the mantissa
+// of a power of two, where they count in units of one (or of 16), and the offset is subtracted; every step
+// is exact.
+__device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b),
+                            *reinterpret_cast<const __half2*>(&c));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// fp16 pair of the 4-bit codes in bits 0-3 of each half (and with kHigh in bits 4-7).
+template <bool kHigh>
+__device__ __forceinline__ uint32_t nibbles_f16(uint32_t w) {
+  if (kHigh) return h2_fma((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u /* 1/16 */, 0xD480D480u /* -72 */);
+  return h2_sub((w & 0x000F000Fu) | 0x64006400u, 0x64086408u /* 1032 */);
+}
+// fp16 pair of the 8-bit codes in the bytes of x that `sel` names (0-3), as __byte_perm selectors 0x4y4x.
+__device__ __forceinline__ uint32_t bytes_f16(uint32_t x, uint32_t sel) {
+  return h2_sub(__byte_perm(x, 0x64646464u, sel), 0x64806480u /* 1152 */);
+}
+// bf16 pair of the 4-bit codes in bits 0-3 of each half.
+__device__ __forceinline__ uint32_t nibbles_bf16(uint32_t w) {
+  const uint32_t v = (w & 0x000F000Fu) | 0x43004300u;
+  const uint32_t k = 0x43084308u;  // 136
+  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&k));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// ------------------------------------------------------------------------------------------------
+// asynchronous copies, each thread's own bytes; src_bytes 0 writes zeros and reads nothing
+// ------------------------------------------------------------------------------------------------
+template <int kBytes>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, uint32_t src_bytes) {
+  if (kBytes == 16) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+  } else {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(src_bytes)
+                 : "memory");
+  }
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+}  // namespace imq

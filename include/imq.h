@@ -463,6 +463,137 @@ imq_status imq_unpacked_gemm_batched(int32_t batch, imq_plan_t *const *plans, co
                                      imq_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------------ */
+/* 5. One decoding step: 4-bit weights for a few tokens, a low-bit cache, attention over it           */
+/* ------------------------------------------------------------------------------------------------ */
+/*
+ * The exact GEMM above multiplies whole matrices.  A model that answers token by token reads every weight
+ * and every cached key and value once for a few rows of work; the calls below keep those in 4 (or 8) bits.
+ * The page has no counterpart: they apply its quantisation rule with p = 1 to small groups, in which
+ * nothing lies outside +-beta, so nothing is unpacked.  For a group of entries x, beta = 2^(bits-1) - 1:
+ *   q = max |x|,  s = (float)beta / q,  step = q / (float)beta,  code = rint_half_even(fp32(x * s))
+ * (imq_rtn_quantize's q, s, Delta and x_int for p = 1).  A group of zeros, or one so small that s would
+ * overflow, has s = step = 1.  A group with a NaN or an infinity has step NaN and codes 0, and sets
+ * IMQ_ERR_NONFINITE in the status word; whatever is computed from it is NaN.  The value of a code is
+ * fp32(code * step).
+ * Storage: code + 2^(bits-1).  At 8 bits a byte each.  At 4 bits eight consecutive codes per 32-bit word,
+ * code e of the eight in bits 4 * (e / 2 + 4 * (e % 2)) .. + 3.
+ * All calls are asynchronous and allocate nothing; argument errors are returned at once and launch nothing.
+ * Pointers must be aligned to their element type unless more is said.
+ */
+
+/*
+ * imq_w4_quantize -- a weight W (K inputs x N output channels, as B in C = A * B) in 4 bits, one step per
+ * output channel and group of `group` consecutive inputs (32, 64 or 128; the last group may be short).
+ * W       device, dtype wt (F32 or BF16).  transW = 0: stored K x N; transW = 1: stored N x K; leading
+ *         dimension ldw.
+ * codes   device, N rows of ldc bytes, 16-byte aligned; ldc a multiple of 16, at least
+ *         64 * ceil(K / IMQ_W4_BLOCK).  A row is blocks of IMQ_W4_BLOCK inputs, 64 bytes each: input r of a
+ *         block is code r % 8 of word 4 * ((r % 32) / 8) + r / 32 of the block.  Inputs behind K are 0.
+ * steps   device, fp32, N x ceil(K / group), leading dimension lds.
+ * Errors: IMQ_ERR_ARG at once; IMQ_ERR_NONFINITE through the status word; IMQ_ERR_UNSUPPORTED for K or N of
+ *         2^31 or more, or K above 8 million with transW = 0.
+ */
+#define IMQ_W4_BLOCK 128
+imq_status imq_w4_quantize(const void *W, imq_dtype wt, int64_t K, int64_t N, int64_t ldw, int32_t transW,
+                           int32_t group, uint8_t *codes, int64_t ldc, float *steps, int64_t lds,
+                           imq_stream_t stream);
+
+/* imq_w4_dequantize -- the values a 4-bit weight stands for, rounded once to wt, into W (K x N, or N x K with
+ * transW = 1, leading dimension ldw).  Arguments as imq_w4_quantize. */
+imq_status imq_w4_dequantize(const uint8_t *codes, int64_t ldc, const float *steps, int64_t lds, int64_t K, int64_t N,
+                             int32_t group, void *W, imq_dtype wt, int64_t ldw, int32_t transW, imq_stream_t stream);
+
+/*
+ * imq_w4_matvec -- Y = X * W for a few tokens and a 4-bit weight:
+ *   Y[m, n] = sum over groups g of steps[n, g] * sum_{k in g} code[n, k] * X[m, k]
+ * with exact products and fp32 sums, rounded once to yt.  The weight is read once per 16 tokens; for many
+ * tokens use the GEMM above.  The order of the sums is fixed: equal inputs give equal bits.
+ * X       device, M x K, dtype xt (F32 or BF16), leading dimension ldx (>= K).  fp32 entries keep all their
+ *         bits.  A non-finite entry gives its token non-finite outputs.
+ * Y       device, M x N, dtype yt (F32 or BF16), leading dimension ldy (>= N).  K = 0 gives zeros.
+ * Errors: IMQ_ERR_ARG; IMQ_ERR_UNSUPPORTED for M above 1 048 560.
+ */
+imq_status imq_w4_matvec(const uint8_t *codes, int64_t ldc, const float *steps, int64_t lds, int64_t K, int64_t N,
+                         int32_t group, const void *X, imq_dtype xt, int64_t M, int64_t ldx, void *Y, imq_dtype yt,
+                         int64_t ldy, imq_stream_t stream);
+
+/*
+ * A paged cache of keys and values (HOST struct of device pointers; the caller owns the memory).  A slot is
+ * page * page_size + position; every slot holds, per head, a key and a value vector of head_dim codes, each
+ * vector one quantisation group.
+ *   k, v    codes, 16-byte aligned: page p starts k_page_stride (v_page_stride) bytes after page p - 1 (a
+ *           multiple of 16); within a page [n_heads][page_size][head_dim * bits / 8], contiguous.
+ *   steps   fp32, 16-byte aligned: page p starts steps_page_stride floats after page p - 1 (a multiple of
+ *           4); within a page [n_heads][page_size][2], the key's step and the value's.
+ * bits 4 or 8.  head_dim 64, 128, 192 or 256; page_size a multiple of 16, at most 65536; at most 65535 heads
+ * (else IMQ_ERR_UNSUPPORTED).
+ */
+typedef struct {
+  uint8_t *k, *v;
+  float *steps;
+  int64_t n_pages;
+  int64_t k_page_stride, v_page_stride, steps_page_stride;
+  int32_t page_size, n_heads, head_dim, bits;
+} imq_kv_cache;
+
+/*
+ * imq_kv_write -- quantises n tokens' keys and values into the cache as it writes them.
+ * K, V    device, dtype xt (F32 or BF16): token i, head h at i * token_stride + h * head_stride (in entries,
+ *         not negative), head_dim consecutive entries.
+ * slots   device int64[n], 8-byte aligned: the slot of each token; a negative one is skipped (padding).
+ *         The slots of one call must differ; of two tokens on one slot it is not defined which one's
+ *         codes and steps are kept.  A slot outside the cache is skipped and sets IMQ_ERR_BOUNDS in the
+ *         status word.
+ */
+imq_status imq_kv_write(const imq_kv_cache *cache, const void *K, int64_t k_token_stride, int64_t k_head_stride,
+                        const void *V, int64_t v_token_stride, int64_t v_head_stride, imq_dtype xt, int64_t n,
+                        const int64_t *slots, imq_stream_t stream);
+
+/*
+ * imq_kv_read -- the values of n slots, rounded once to yt, into K and V (either may be NULL), addressed as
+ * in imq_kv_write.  Slots may repeat.  The outputs of a negative slot are left as they were, those of a slot
+ * outside the cache too, which sets IMQ_ERR_BOUNDS.
+ */
+imq_status imq_kv_read(const imq_kv_cache *cache, const int64_t *slots, int64_t n, void *K, int64_t k_token_stride,
+                       int64_t k_head_stride, void *V, int64_t v_token_stride, int64_t v_head_stride, imq_dtype yt,
+                       imq_stream_t stream);
+
+/* imq_paged_attention_workspace -- device bytes imq_paged_attention needs for these sizes (may be 0). */
+imq_status imq_paged_attention_workspace(const imq_kv_cache *cache, int64_t batch, int32_t n_q_heads, int64_t max_len,
+                                         size_t *bytes);
+
+/*
+ * imq_paged_attention -- attention of one query token per sequence over the cache.  With t over the tokens
+ * 0 .. seq_lens[b] - 1 of sequence b, and the key head h / (n_q_heads / n_heads) of query head h:
+ *   s_t = scale * sum_d Q[b, h, d] * key_t[d],  out[b, h, :] = sum_t softmax(s)_t * value_t,
+ *   lse[b, h] = log sum_t exp(s_t)
+ * Scores, softmax statistics and sums are fp32; codes enter the products exactly, queries with 22 bits
+ * (and 2^-39 of the largest entry at the least), probabilities times the values' steps with 22 bits (and
+ * 2^-40 of the largest at the least).  The order of the sums is fixed: equal inputs give equal bits.
+ * Q           device, dtype qt (F32 or BF16): sequence b, head h at b * q_batch_stride + h * q_head_stride, head_dim
+ *             consecutive entries.  A non-finite query gives NaN.
+ * block_table device int32, batch rows of table_stride entries: entry j of a row is the page of tokens
+ *             j * page_size .. + page_size - 1.  table_width entries of a row may be read; only those that
+ *             cover a sequence's tokens are.
+ * seq_lens    device int32[batch].  A sequence without tokens (0 or less) has out 0 and lse -infinity.
+ * max_len     no sequence is longer (at most table_width * page_size); it sizes the launch.  A longer sequence
+ *             has out and lse NaN and sets IMQ_ERR_BOUNDS in the status word; so has one whose page lies outside
+ *             the cache.
+ * out         device, dtype ot (F32 or BF16), addressed as Q.   lse: device fp32 or NULL, row b at
+ *             b * lse_batch_stride.
+ * workspace   device, 16-byte aligned, at least imq_paged_attention_workspace bytes (IMQ_ERR_BUFFER otherwise); need
+ *             not be initialised.  Calls whose executions overlap, and graphs that replay at the same time,
+ *             need workspaces of their own.
+ * n_q_heads must be a multiple of the cache's heads (IMQ_ERR_ARG).
+ */
+imq_status imq_paged_attention(const imq_kv_cache *cache, const void *Q, imq_dtype qt, int64_t q_batch_stride,
+                               int64_t q_head_stride, int64_t batch, int32_t n_q_heads, const int32_t *block_table,
+                               int64_t table_stride, int64_t table_width, const int32_t *seq_lens, int64_t max_len,
+                               float scale, void *out, imq_dtype ot, int64_t o_batch_stride, int64_t o_head_stride,
+                               float *lse, int64_t lse_batch_stride, void *workspace, size_t workspace_bytes,
+                               imq_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------------ */
 /* Status                                                                                            */
 /* ------------------------------------------------------------------------------------------------ */
 /* Synchronises the stream, returns the device status word of the current device and, when clear is
