@@ -5,24 +5,33 @@
 // with ck, cv the codes and dk, dv the steps of the cache.
 //
 // Bound: the cache is read once, 2 D bits / 8 + 8 bytes a token and key head, for 4 G D operations of G
-// query heads -- memory, far below the tensor cores' rate, but above what fp32 units do at 8 query heads a
-// key head.  So the products run on the warp-level tensor-core instruction (16 x 8 x 16, fp16 with fp32
-// sums), whose operands are registers: the codes go from the copy to the operand without another trip
-// through shared memory, and every fp16 value on the way is exact.
-//   - Codes in -127..127 are exact in fp16.
-//   - A query is scaled by a power of two to put its largest entry near 2^15 and cut into two fp16 parts, 22
-//     bits together.  With up to 8 query heads a key head both parts share one 16-row operand (rows g and
-//     g + 8), so the second part costs no further instruction; 9 to 16 heads take a product per part.
-//   - A probability is weighted with its value's step relative to the largest step so far, scaled by 2^15
-//     and cut into two fp16 parts in the same way.  The running maxima of the scores and of the steps
-//     rescale the sums when they grow.
+// query heads -- memory, far below the tensor cores' rate, but above what the fp32 units do at 8 query heads a
+// key head.  So both products run on warp-level tensor-core instructions, whose operands are registers: the
+// codes go from the copy to the operand without another trip through shared memory.
+//   - q * k runs on integers, exactly: a query row is scaled so that its largest entry becomes 2^23 - 2^15 - 2^7
+//     and rounded to an integer of three digits of radix 256 in -128 .. 127 (the unpacking of this library,
+//     applied to the query), and the stored bytes or nibbles are the other operand as they lie, offset and
+//     all: the offset times the sum of a row's digits is what the sums start from.  8-bit codes need no
+//     conversion, 4-bit codes three instructions for eight.  Rows g and g + 8 of one 16-row operand hold the
+//     first two digits of up to 8 query heads, a second operand the third; for 9 to 16 heads each digit has
+//     an operand.
+//   - p * v runs on fp16 with fp32 sums: codes are exact in fp16; a probability times its value's step, in units
+//     of the largest step so far and of 2^-11, is cut into two fp16 parts, 22 bits together.  With up to 8
+//     query heads both parts share one 16-row operand, so the second costs no further instruction.
 // The inner axis of a product may be permuted at will if both operands agree, so a lane's 16 (8, 4) bytes
 // of a key are contiguous ones, and a lane's bytes of four values make the columns of the second product.
 //
-// Split: a CTA of four warps takes a chunk of one sequence and one key head; its warps take tiles of 16
-// tokens in turn, each with its own ring of asynchronous copies (every lane copies what it will use
-// itself, so a tile waits for no barrier but the warp's).  The warps join in shared memory; chunks of one
-// sequence join in k_attn_join from partial sums in the workspace, in a fixed order.
+// The softmax keeps a reference instead of the running maximum: it is raised (and the sums rescaled) only when a
+// score exceeds it by 4 (a weight 16, the room that fp16 leaves above 2^11), so most tiles need no exchange
+// between lanes.
+//
+// Split: the work of all sequences and key heads lies in one line of units of 64 tokens, cut into equal parts, one
+// for each CTA that the SMs hold at once; so lengths may differ as they will.  A CTA's four warps take tiles
+// of 16 tokens in turn, each with its own ring of asynchronous copies (every lane copies what it will use
+// itself, so a tile waits for no barrier but the warp's), and join in shared memory.  Rows that several CTAs
+// share join in k_attn_join from partial sums in the workspace, in a fixed order.
+#include <type_traits>
+
 #include "lowbit.cuh"
 #include "internal.h"
 
@@ -30,33 +39,35 @@ namespace imq {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kTile = 16;      // tokens of a warp's tile
-constexpr int kStages = 4;     // tiles in a warp's ring
+constexpr int kTile = 16;              // tokens of a warp's tile; it lies in one page (pages are multiples of it)
+constexpr int kUnit = kWarps * kTile;  // tokens: the grain of the split
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kPScale = 32768.f;
-constexpr float kStepFloor = 1e-30f;
+constexpr float kSlack = 4.f;          // how far, in powers of two, a weight may exceed the reference's
+constexpr float kPScale = 2048.f;      // unit of the weights in fp16: 2^15 is the largest
+constexpr float kStepFloor = 1e-30f;   // the unit of the steps starts here
+constexpr float kQMax = 8355711.f;     // 127 * 65536 + 127 * 256 + 127
 
 struct AttnArgs {
   imq_kv_cache c;
   const void* Q;
   int64_t q_batch, q_head;
-  int q_bf16;
-  int group;       // query heads of a key head
-  int head_chunks; // blocks of up to 8 * kM query heads per key head
+  int q_bf16, q_vec;  // q_vec: four entries of a row may be read at once
+  int group;          // query heads of a key head
+  int head_chunks;    // blocks of up to 8 * kM query heads per key head
   const int32_t* table;
   int64_t table_stride;
   const int32_t* lens;
-  int64_t limit;   // longest sequence the call covers
-  int64_t chunk;   // tokens of a split
-  int splits;
+  int batch;
+  int limit;          // longest sequence the call covers
+  int ctas;           // of k_attn
   float scale;
   void* out;
   int64_t o_batch, o_head;
   int o_bf16;
   float* lse;
   int64_t lse_batch;
-  float* part;     // [batch][split][query head][D]
-  float2* ml;      // [batch][split][query head]: maximum (in log2 units) and sum
+  float* part;        // [CTA][2][head of the row][D]: sums of rows that several CTAs share
+  float2* ml;         // [CTA][2][head of the row]: reference (a power of two's exponent) and sum of the weights
   int32_t* status;
 };
 
@@ -68,10 +79,10 @@ struct Pieces {
   static constexpr int n16 = kBytes / 16, n8 = kBytes % 16 / 8, n4 = kBytes % 8 / 4;
 };
 
-// Copies lane `i` of kShare lanes' pieces of the vector at src to dst + 16 * lane, laid out so that each
-// piece of a warp is 32 consecutive slots.
+// Copies lane `i` of kShare lanes' pieces of the vector at src to dst, laid out so that each piece of a warp
+// is 32 consecutive slots; `on` false writes zeros and reads nothing.
 template <typename P, int kShare>
-__device__ __forceinline__ void copy_pieces(uint32_t dst, int lane, const uint8_t* src, int i, uint32_t on) {
+__device__ __forceinline__ void copy_pieces(uint32_t dst, int lane, const uint8_t* src, int i, bool on) {
 #pragma unroll
   for (int j = 0; j < P::n16; ++j) cp_async<16>(dst + (j * 32 + lane) * 16, src + (j * kShare + i) * 16, on ? 16u : 0u);
   if (P::n8) cp_async<8>(dst + P::n16 * 512 + lane * 8, src + P::n16 * kShare * 16 + i * 8, on ? 8u : 0u);
@@ -103,14 +114,35 @@ __device__ __forceinline__ int word_byte(int i, int l) {
   return base + l * 4;
 }
 
-__device__ __forceinline__ float load_q(const AttnArgs& a, int64_t at) {
-  return a.q_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.Q)[at]) : static_cast<const float*>(a.Q)[at];
+// Four consecutive entries; vec: they are aligned to their size together.
+__device__ __forceinline__ void load4(const float* p, bool vec, float (&x)[4]) {
+  if (vec) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(p));
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = p[j];
+  }
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, bool vec, float (&x)[4]) {
+  if (vec) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = __bfloat162float(p[j]);
+  }
 }
 __device__ __forceinline__ void store_out(const AttnArgs& a, int64_t at, float v) {
   if (a.o_bf16)
     static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
   else
     static_cast<float*>(a.out)[at] = v;
+}
+// Four consecutive entries of out, aligned as they may be.
+__device__ __forceinline__ void store_out4(const AttnArgs& a, int64_t at, const float4& v) {
+  store_out(a, at, v.x), store_out(a, at + 1, v.y), store_out(a, at + 2, v.z), store_out(a, at + 3, v.w);
 }
 
 // x as two fp16 parts (hi, lo), pairs packed.
@@ -122,389 +154,648 @@ __device__ __forceinline__ void split_f16(float x0, float x1, uint32_t* hi, uint
   *lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
-// kM 16-row operands per product: 1 for up to 8 query heads a key head (rows g: first parts, rows g + 8:
-// second parts), 2 for 9 to 16 (an operand per part).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float minus_inf() { return __uint_as_float(0xFF800000u); }
+__device__ __forceinline__ float quiet_nan() { return __uint_as_float(0x7FC00000u); }
+
+// Units of a sequence (0 for one that has no tokens or that the call does not cover).
+__device__ __forceinline__ uint32_t units_of(const AttnArgs& a, int len) {
+  return len <= 0 || len > a.limit ? 0u : (uint32_t)(len + kUnit - 1) / kUnit;
+}
+// The parts of the line: `all` units over `n` CTAs, the first all % n take one more.
+struct Parts {
+  uint32_t each, more;
+  __device__ __forceinline__ Parts(uint32_t all, uint32_t n) : each(all / n), more(all % n) {}
+  __device__ __forceinline__ uint32_t begin(uint32_t i) const { return each * i + min(i, more); }
+  __device__ __forceinline__ uint32_t cta_of(uint32_t u) const {
+    const uint32_t big = more * (each + 1);
+    return u < big ? u / (each + 1) : more + (u - big) / each;
+  }
+};
+
+// kM: 1 for up to 8 query heads a key head, 2 for 9 to 16.
 template <int kBits, int kD, int kM>
 struct Shape {
   using KP = Pieces<kBits, kD, 4>;
   using VP = Pieces<kBits, kD, 8>;
-  static constexpr int kSteps = kD / 16;                       // inner steps of q * k
-  static constexpr int kCols = kD / 8;                         // 8-column blocks of p * v
-  static constexpr int kKeyBytes = kTile * KP::kBytes * 4;     // of a tile
-  static constexpr int kTileBytes = 2 * kKeyBytes + kTile * 8; // keys, values, steps
-  static constexpr int kRing = kStages * kTileBytes;           // of a warp
+  static constexpr int kRow = kD * kBits / 8;
+  static constexpr int kSteps = kD / 32;               // inner steps of q * k
+  static constexpr int kCols = kD / 8;                 // 8-column blocks of p * v
+  static constexpr int kTileBytes = 32 * kRow + 128;   // keys, values, steps of 16 tokens
+  // about 13 KB for a warp's ring: 16 warps an SM have 130 KB of copies under way
+  static constexpr int kStages = 13000 / kTileBytes < 2 ? 2 : 13000 / kTileBytes > 8 ? 8 : 13000 / kTileBytes;
+  static constexpr int kRing = kStages * kTileBytes;
+  static constexpr int kPerSm = kD <= 128 ? 4 : 2;     // CTAs an SM, by the registers of the sums
   static constexpr int kHeads = 8 * kM;
-  static constexpr int kQBytes = kSteps * 32 * 16 * kM;        // query operands
-  static constexpr int kJoin = kWarps * kHeads * (kD + 4) * 4; // the warps' sums, over the ring
+  static constexpr int kQOps = kM + 1;                 // operands of the digits, 512 bytes each a step
+  static constexpr int kQBytes = kSteps * kQOps * 512;
+  static constexpr int kPad = kD + 4;
+  static constexpr int kJoin = kWarps * kHeads * kPad * 4;  // the warps' sums, over the ring
   static constexpr int kSmem = kQBytes + (kWarps * kRing > kJoin ? kWarps * kRing : kJoin);
 };
 
+// The query operands of one row block: `load` reads four entries of a head.
+// Entry (step, operand, lane) is {row g at the step's first four inner positions of column c, row g + 8 at them,
+// row g at the second four, row g + 8}; the positions are the ones whose codes a lane's words hold.
+template <int kBits, int kD, int kM, typename Load>
+__device__ __forceinline__ void prepare_query(uint4* qs, int32_t (*s_dig)[8 * kM], float* s_mul, int heads, float scale, int warp,
+                                              int lane, Load load) {
+  using S = Shape<kBits, kD, kM>;
+  uint8_t* const bytes = reinterpret_cast<uint8_t*>(qs);
+  // a warp takes a head: lane i its entries 4i .. 4i + 3 (and 128 further on)
+  constexpr int kParts = (kD + 127) / 128;
+  for (int h = warp; h < 8 * kM; h += kWarps) {
+    float x[kParts][4] = {};
+    uint32_t key = 0;
+#pragma unroll
+    for (int p = 0; p < kParts; ++p)
+      if (h < heads && 4 * lane + 128 * p < kD) {
+        load(h, 4 * lane + 128 * p, x[p]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) key = max(key, abs_key(x[p][j]));
+      }
+    key = __reduce_max_sync(0xffffffffu, key);
+    // r * max = kQMax but for a rounding; a row of (almost) zeros, and one that is not finite (its scores' factor is
+    // NaN), have digits of 0
+    const float top = __uint_as_float(key);
+    const bool use = key_finite(key) && top > 1e-30f;
+    const float r = use ? __fdiv_rn(kQMax, top) : 0.f;
+    if (lane == 0) s_mul[h] = !key_finite(key) ? quiet_nan() : use ? scale * kLog2e * __fdiv_rn(top, kQMax) : 0.f;
+    int32_t sum[3] = {};
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+      const int d = 4 * lane + 128 * p;
+      if (d >= kD) continue;
+      uint32_t dig[3] = {};  // this lane's four entries, a byte each
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        int32_t v = use ? __float2int_rn(x[p][j] * r) : 0;
+        v = max(-8355711, min(8355711, v));
+#pragma unroll
+        for (int k = 2; k >= 0; --k) {  // third, second, first digit
+          const int32_t low = (int32_t)(int8_t)(v & 255);
+          dig[k] |= (uint32_t)(low & 255) << (8 * j);
+          sum[k] += low;
+          v = (v - low) >> 8;
+        }
+      }
+      // where the four entries go: lane column, step and place of their codes
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        // kM = 1: operand 0 holds the first digit in row g and the second in row g + 8, operand 1 the third in row g;
+        // kM = 2: an operand a digit, heads g and g + 8
+        const int op = kM == 1 ? k / 2 : k, high = kM == 1 ? k % 2 : h / 8, g = kM == 1 ? h : h % 8;
+        if constexpr (kBits == 8) {
+          // four entries are one word of a key: word w of column c; inner step w / 2, first or second four
+          const int at = d;
+          int c, w;
+          if (at < S::KP::n16 * 64) c = at % 64 / 16, w = at / 64 * 4 + at % 16 / 4;
+          else c = (at - S::KP::n16 * 64) / 8, w = S::KP::n16 * 4 + (at - S::KP::n16 * 64) % 8 / 4;
+          reinterpret_cast<uint32_t*>(bytes)[((w / 2 * S::kQOps + op) * 32 + g * 4 + c) * 4 + (w % 2) * 2 + high] = dig[k];
+        } else {
+          // a word of a key is eight entries, its even nibbles (codes 0, 4, 1, 5) the first four positions of the
+          // step and its odd ones (codes 2, 6, 3, 7) the second; these four entries are codes 0-3 or 4-7
+          const int at = d / 2;  // byte of the vector (a multiple of 2)
+          int c, w;
+          if (at < S::KP::n16 * 64) c = at % 64 / 16, w = at / 64 * 4 + at % 16 / 4;
+          else c = (at - S::KP::n16 * 64) / 8, w = S::KP::n16 * 4 + (at - S::KP::n16 * 64) % 8 / 4;
+          const int e = d % 8 / 4;
+          uint8_t* const to = bytes + (((w * S::kQOps + op) * 32 + g * 4 + c) * 4 + high) * 4;
+          to[e] = dig[k] & 255, to[e + 2] = dig[k] >> 8 & 255;            // codes 0 and 1 (4 and 5)
+          to[8 + e] = dig[k] >> 16 & 255, to[8 + e + 2] = dig[k] >> 24;   // codes 2 and 3 (6 and 7)
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      sum[k] = __reduce_add_sync(0xffffffffu, sum[k]);
+      if (lane == 0) s_dig[k][h] = -(1 << (kBits - 1)) * sum[k];
+    }
+  }
+}
+
 template <int kBits, int kD, int kM>
-__global__ void __launch_bounds__(kWarps * 32) k_attn(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_attn(const __grid_constant__ AttnArgs a) {
   using S = Shape<kBits, kD, kM>;
   using KP = typename S::KP;
   using VP = typename S::VP;
+  constexpr int kStages = S::kStages, kRow = S::kRow;
   extern __shared__ __align__(16) uint8_t smem[];
   uint4* const qs = reinterpret_cast<uint4*>(smem);
   uint8_t* const ring = smem + S::kQBytes;
   __shared__ float s_mul[S::kHeads];
+  __shared__ int32_t s_dig[3][S::kHeads];
   __shared__ float s_m[kWarps][S::kHeads], s_l[kWarps][S::kHeads];
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-  const int b = blockIdx.z, split = blockIdx.x;
-  const int kv = blockIdx.y / a.head_chunks, h0 = kv * a.group + (blockIdx.y % a.head_chunks) * S::kHeads;
-  const int heads = min(S::kHeads, (kv + 1) * a.group - h0);
-  const int q_heads = a.c.n_heads * a.group;
-  const int64_t len = a.lens[b];
-  const bool over = len > a.limit;
-  const int64_t begin = split * a.chunk, end = over ? 0 : min(len, begin + a.chunk);
+  const uint32_t rows = a.c.n_heads * a.head_chunks;
   asm volatile("griddepcontrol.launch_dependents;");
+  // the last rows of the operands that hold no digit stay zero
+  for (int i = threadIdx.x; i < S::kQBytes / 16; i += kWarps * 32) qs[i] = make_uint4(0u, 0u, 0u, 0u);
 
-  if (begin >= end) {  // nothing here; a sequence without tokens, or one longer than the call covers, is answered
-    if (over && split == 0 && threadIdx.x == 0) set_status(a.status, IMQ_ERR_BOUNDS);
-    const float nan = __uint_as_float(0x7FC00000u), minus_inf = __uint_as_float(0xFF800000u);
-    if (a.splits > 1) {
-      if (threadIdx.x < heads)
-        a.ml[((int64_t)b * a.splits + split) * q_heads + h0 + threadIdx.x] = make_float2(minus_inf, over ? nan : 0.f);
+  // ---- this CTA's part of the line: units u0 .. u1 - 1 (every warp finds it by itself)
+  uint32_t all = 0;
+  for (int i = lane; i < a.batch; i += 32) all += units_of(a, __ldg(a.lens + i));
+  all = __reduce_add_sync(0xffffffffu, all) * rows;
+  // sequences without tokens, and those longer than the call covers, are answered here
+  for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+    const int len = __ldg(a.lens + b);
+    if (units_of(a, len)) continue;
+    const bool over = len > a.limit;
+    if (over && threadIdx.x == 0) set_status(a.status, IMQ_ERR_BOUNDS);
+    for (int i = threadIdx.x; i < a.c.n_heads * a.group * kD; i += kWarps * 32)
+      store_out(a, b * a.o_batch + i / kD * a.o_head + i % kD, over ? quiet_nan() : 0.f);
+    if (a.lse)
+      for (int i = threadIdx.x; i < a.c.n_heads * a.group; i += kWarps * 32)
+        a.lse[b * a.lse_batch + i] = over ? quiet_nan() : minus_inf();
+  }
+  const uint32_t ctas = min((uint32_t)a.ctas, all);
+  if (blockIdx.x >= ctas) return;
+  const Parts parts(all, ctas);
+  uint32_t u0 = parts.begin(blockIdx.x);
+  const uint32_t u1 = parts.begin(blockIdx.x + 1);
+  // the sequence that u0 lies in, and the units before it
+  int b = 0;
+  uint32_t base = 0;
+  for (int i0 = 0;; i0 += 32) {
+    const uint32_t mine = i0 + lane < a.batch ? units_of(a, __ldg(a.lens + i0 + lane)) * rows : 0u;
+    uint32_t sum = mine;  // of the lanes up to this one
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += x;
+    }
+    const unsigned behind = __ballot_sync(0xffffffffu, base + sum > u0);
+    if (behind || i0 + 32 >= a.batch) {
+      const int l = behind ? __ffs(behind) - 1 : 31;
+      b = i0 + l;
+      base += __shfl_sync(0xffffffffu, sum - mine, l);
+      break;
+    }
+    base += __shfl_sync(0xffffffffu, sum, 31);
+  }
+
+  __syncthreads();  // the operands are cleared
+
+  // ---- a row's part after the other
+  while (u0 < u1) {
+    const int len = __ldg(a.lens + b);
+    const uint32_t per_row = units_of(a, len);
+    if (u0 - base >= per_row * rows) {
+      base += per_row * rows;
+      ++b;
+      continue;
+    }
+    const uint32_t row = (u0 - base) / per_row, unit = (u0 - base) % per_row, take = min(per_row - unit, u1 - u0);
+    u0 += take;
+    const int begin = (int)(unit * kUnit), end = min(len, begin + (int)(take * kUnit)), first = begin + warp * kTile;
+    const int kv = row / a.head_chunks, h0 = kv * a.group + row % a.head_chunks * S::kHeads;
+    const int heads = min(S::kHeads, (kv + 1) * a.group - h0);
+    const int32_t* const table = a.table + b * a.table_stride;
+    const int n_tiles = first < end ? (end - first + kUnit - 1) / kUnit : 0;
+
+    // Page and place (first token's position in it) of the warp's tiles i .. i + 31, one a lane.
+    auto locate = [&](int i, int32_t& page, uint32_t& place) {
+      i += lane;
+      page = -1, place = 0;
+      if (i < n_tiles) {
+        const uint32_t t = first + i * kUnit, j = t / (uint32_t)a.c.page_size;
+        page = __ldg(table + j);
+        place = t - j * (uint32_t)a.c.page_size;
+        if (page >= a.c.n_pages) page = -1;
+      }
+    };
+    int32_t page_now, page_next;
+    uint32_t place_now, place_next;
+    locate(0, page_now, place_now);
+    locate(32, page_next, place_next);
+
+    // ---- the warp's copies
+    const uint32_t mine = smem_addr(ring) + warp * S::kRing;
+    const uint8_t* const k_base = a.c.k + (int64_t)kv * a.c.page_size * kRow;
+    const uint8_t* const v_base = a.c.v + (int64_t)kv * a.c.page_size * kRow;
+    const float* const s_base = a.c.steps + (int64_t)kv * a.c.page_size * 2;
+    bool bad = false;
+    uint32_t fill = mine;  // the stage that is filled next
+    auto issue = [&](int i) {
+      if (i < n_tiles) {
+        if ((i & 31) == 0 && i > 0) {
+          page_now = page_next, place_now = place_next;
+          locate(i + 32, page_next, place_next);
+        }
+        const int32_t page = __shfl_sync(0xffffffffu, page_now, i & 31);
+        const uint32_t place = __shfl_sync(0xffffffffu, place_now, i & 31);
+        const int left = end - (first + i * kUnit);
+        const uint64_t p = max(page, 0);
+        const uint8_t* kp = k_base + p * (uint64_t)a.c.k_page_stride + place * (uint32_t)kRow;
+        const uint8_t* vp = v_base + p * (uint64_t)a.c.v_page_stride + place * (uint32_t)kRow;
+        const float* sp = s_base + p * (uint64_t)a.c.steps_page_stride + place * 2u;
+        if (left >= kTile && page >= 0) {
+          kp += g * kRow, vp += 2 * c * kRow;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) copy_pieces<KP, 4>(fill + j * 8 * kRow, lane, kp + 8 * j * kRow, c, true);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            copy_pieces<VP, 8>(fill + (16 + 4 * j) * kRow, lane, vp + (8 * (j >> 1) + (j & 1)) * kRow, g, true);
+          if (lane < 8) cp_async<16>(fill + 32 * kRow + lane * 16, sp + lane * 4, 16u);
+        } else {
+          // the end of the sequence, or a page outside the cache: what is not read is zero-filled (steps of 0: no
+          // stale value meets a weight of 0), with an address that is not read either
+          const int valid = page < 0 ? 0 : min(left, kTile);
+          bad |= page < 0;
+#pragma unroll 1
+          for (int j = 0; j < 2; ++j) {
+            const int t = 8 * j + g;
+            copy_pieces<KP, 4>(fill + j * 8 * kRow, lane, kp + (t < valid ? t : 0) * kRow, c, t < valid);
+          }
+#pragma unroll 1
+          for (int j = 0; j < 4; ++j) {
+            const int t = 8 * (j >> 1) + 2 * c + (j & 1);
+            copy_pieces<VP, 8>(fill + (16 + 4 * j) * kRow, lane, vp + (t < valid ? t : 0) * kRow, g, t < valid);
+          }
+          const int n = min(max(valid - 2 * lane, 0), 2);
+          if (lane < 8) cp_async<16>(fill + 32 * kRow + lane * 16, sp + (n ? lane * 4 : 0), 8u * n);
+        }
+        fill = fill + S::kTileBytes == mine + S::kRing ? mine : fill + S::kTileBytes;
+      }
+      cp_async_commit();
+    };
+#pragma unroll 1
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
+
+    // ---- the query operands, while the first copies are under way
+    const int64_t q0 = b * a.q_batch + h0 * a.q_head;
+    auto query = [&](const auto* Q, auto vec) {
+      prepare_query<kBits, kD, kM>(qs, s_dig, s_mul, heads, a.scale, warp, lane,
+                                   [&](int h, int d, float(&x)[4]) { load4(Q + q0 + h * a.q_head + d, vec, x); });
+    };
+    if (a.q_bf16) {
+      const auto* Q = static_cast<const __nv_bfloat16*>(a.Q);
+      if (a.q_vec) query(Q, std::true_type()); else query(Q, std::false_type());
     } else {
-      for (int i = threadIdx.x; i < heads * kD; i += kWarps * 32)
-        store_out(a, b * a.o_batch + (h0 + i / kD) * a.o_head + i % kD, over ? nan : 0.f);
-      if (a.lse && threadIdx.x < heads) a.lse[b * a.lse_batch + h0 + threadIdx.x] = over ? nan : minus_inf;
+      const auto* Q = static_cast<const float*>(a.Q);
+      if (a.q_vec) query(Q, std::true_type()); else query(Q, std::false_type());
+    }
+    __syncthreads();
+    float mul[kM];
+    int32_t start[3][kM];  // what the digits' sums start from
+#pragma unroll
+    for (int r = 0; r < kM; ++r) {
+      mul[r] = s_mul[g + 8 * r];
+#pragma unroll
+      for (int k = 0; k < 3; ++k) start[k][r] = s_dig[k][g + 8 * r];
+    }
+
+    // ---- the warp's tiles
+    float o[S::kCols][4] = {};
+    float m[kM], l[kM], vref = kStepFloor, winv = kPScale / kStepFloor;
+#pragma unroll
+    for (int r = 0; r < kM; ++r) m[r] = minus_inf(), l[r] = 0.f;
+    const uint8_t* tile = ring + warp * S::kRing;
+
+#pragma unroll 1
+    for (int i = 0; i < n_tiles; ++i) {
+      cp_async_wait<kStages - 2>();
+      __syncwarp();  // the steps were copied by eight lanes; and every lane is done with the tile that is overwritten now
+      issue(i + kStages - 1);
+      // ---- scores of two blocks of eight tokens; this lane's tokens are 2c, 2c + 1, 2c + 8, 2c + 9, its heads g
+      // (and g + 8)
+      float p[kM][4];
+      {
+        int32_t acc[2][S::kQOps][4];
+        uint32_t w[2][KP::kBytes / 4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) read_pieces<KP>(tile + j * 8 * kRow, lane, w[j]);
+#pragma unroll
+        for (int st = 0; st < S::kSteps; ++st) {
+#pragma unroll
+          for (int op = 0; op < S::kQOps; ++op) {
+            const uint4 q = qs[(st * S::kQOps + op) * 32 + lane];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t b0 = kBits == 8 ? w[j][kBits == 8 ? 2 * st : 0] : w[j][kBits == 8 ? 0 : st] & 0x0F0F0F0Fu;
+              const uint32_t b1 = kBits == 8 ? w[j][kBits == 8 ? 2 * st + 1 : 0] : w[j][kBits == 8 ? 0 : st] >> 4 & 0x0F0F0F0Fu;
+              int32_t(&d)[4] = acc[j][op];
+              if (st == 0) {
+                const int32_t c0 = kM == 1 ? (op == 0 ? start[0][0] : start[2][0]) : start[op][0];
+                const int32_t c2 = kM == 1 ? (op == 0 ? start[1][0] : 0) : start[op][kM - 1];
+                mma_s8u8(d, q.x, q.y, q.z, q.w, b0, b1, c0, c0, c2, c2);
+              } else {
+                mma_s8u8(d, q.x, q.y, q.z, q.w, b0, b1, d[0], d[1], d[2], d[3]);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < kM; ++r)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const auto& x = acc[j >> 1];
+            const int32_t d0 = kM == 1 ? x[0][j & 1] : x[0][2 * r + (j & 1)];
+            const int32_t d1 = kM == 1 ? x[0][2 + (j & 1)] : x[kM - 1][2 * r + (j & 1)];
+            const int32_t d2 = kM == 1 ? x[1][j & 1] : x[kM][2 * r + (j & 1)];
+            p[r][j] = fmaf((float)(d0 * 256 + d1), 256.f, (float)d2);
+          }
+      }
+      const float4 st0 = *reinterpret_cast<const float4*>(tile + 32 * kRow + c * 16);
+      const float4 st1 = *reinterpret_cast<const float4*>(tile + 32 * kRow + 64 + c * 16);
+      const float ks[4] = {st0.x, st0.z, st1.x, st1.z}, vs[4] = {st0.y, st0.w, st1.y, st1.w};
+      const int left = end - (first + i * kUnit);
+      bool raise = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3])) > vref;
+#pragma unroll
+      for (int r = 0; r < kM; ++r)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[r][j] *= ks[j] * mul[r];
+      if (left < kTile) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (8 * (j >> 1) + 2 * c + (j & 1) >= left) {
+#pragma unroll
+            for (int r = 0; r < kM; ++r) p[r][j] = minus_inf();
+          }
+      }
+#pragma unroll
+      for (int r = 0; r < kM; ++r) raise |= fmaxf(fmaxf(p[r][0], p[r][1]), fmaxf(p[r][2], p[r][3])) > m[r] + kSlack;
+      if (__any_sync(0xffffffffu, raise)) {
+        // new references, the largest so far, and the sums in their units
+        float vmax = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3])), fix[kM];
+        vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
+        vmax = fmaxf(fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2)), vref);
+        const float ratio = vref / vmax;
+        vref = vmax, winv = kPScale / vmax;
+#pragma unroll
+        for (int r = 0; r < kM; ++r) {
+          float top = fmaxf(fmaxf(p[r][0], p[r][1]), fmaxf(p[r][2], p[r][3]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)), m[r]);
+          const float alpha = top == minus_inf() ? 1.f : ex2(m[r] - top);  // (no score yet but NaN)
+          m[r] = top;
+          l[r] *= alpha;
+          fix[r] = alpha * ratio;
+        }
+#pragma unroll
+        for (int n = 0; n < S::kCols; ++n) {
+          o[n][0] *= fix[0], o[n][1] *= fix[0];
+          o[n][2] *= fix[kM - 1], o[n][3] *= fix[kM - 1];
+        }
+      }
+      uint32_t hi[kM][2], lo[kM][2];  // weights as operands
+      float vw[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) vw[j] = vs[j] * winv;
+#pragma unroll
+      for (int r = 0; r < kM; ++r) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          p[r][j] = ex2(p[r][j] - m[r]);
+          l[r] += p[r][j];
+          p[r][j] *= vw[j];
+        }
+        split_f16(p[r][0], p[r][1], &hi[r][0], &lo[r][0]);
+        split_f16(p[r][2], p[r][3], &hi[r][1], &lo[r][1]);
+      }
+      auto product = [&](float (&acc)[4], uint32_t b0, uint32_t b1) {
+        if (kM == 1) {
+          mma_f16(acc, hi[0][0], lo[0][0], hi[0][1], lo[0][1], b0, b1);
+        } else {
+          mma_f16(acc, hi[0][0], hi[kM - 1][0], hi[0][1], hi[kM - 1][1], b0, b1);
+          mma_f16(acc, lo[0][0], lo[kM - 1][0], lo[0][1], lo[kM - 1][1], b0, b1);
+        }
+      };
+      uint32_t w[4][VP::kBytes / 4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) read_pieces<VP>(tile + (16 + 4 * j) * kRow, lane, w[j]);
+#pragma unroll
+      for (int n = 0; n < VP::kBytes / 4; ++n) {
+        if constexpr (kBits == 8) {
+          const uint32_t x0 = __byte_perm(w[0][n], w[1][n], 0x5140), x1 = __byte_perm(w[0][n], w[1][n], 0x7362);
+          const uint32_t y0 = __byte_perm(w[2][n], w[3][n], 0x5140), y1 = __byte_perm(w[2][n], w[3][n], 0x7362);
+          product(o[4 * n], bytes_f16(x0, 0x4140), bytes_f16(y0, 0x4140));
+          product(o[4 * n + 1], bytes_f16(x0, 0x4342), bytes_f16(y0, 0x4342));
+          product(o[4 * n + 2], bytes_f16(x1, 0x4140), bytes_f16(y1, 0x4140));
+          product(o[4 * n + 3], bytes_f16(x1, 0x4342), bytes_f16(y1, 0x4342));
+        } else {
+          // byte k of a word holds codes (0, 2), (4, 6), (1, 3), (5, 7) in its low and high half
+          constexpr int kSel[4] = {0x0400, 0x0501, 0x0602, 0x0703}, kLow[4] = {0, 4, 1, 5}, kUp[4] = {2, 6, 3, 7};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t x = __byte_perm(w[0][n], w[1][n], kSel[k]), y = __byte_perm(w[2][n], w[3][n], kSel[k]);
+            product(o[8 * n + kLow[k]], nibbles_f16<false>(x), nibbles_f16<false>(y));
+            product(o[8 * n + kUp[k]], nibbles_f16<true>(x), nibbles_f16<true>(y));
+          }
+        }
+      }
+      tile = tile + S::kTileBytes == ring + (warp + 1) * S::kRing ? ring + warp * S::kRing : tile + S::kTileBytes;
+    }
+    cp_async_wait<0>();
+
+    // ---- join the warps' sums
+    bad = __any_sync(0xffffffffu, bad);
+    if (bad && lane == 0) set_status(a.status, IMQ_ERR_BOUNDS);
+#pragma unroll
+    for (int r = 0; r < kM; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      if (c == 0) s_m[warp][g + 8 * r] = m[r], s_l[warp][g + 8 * r] = bad ? quiet_nan() : l[r];
+    }
+    __syncthreads();  // the rings are done with: they hold the sums from here
+    float* const sums = reinterpret_cast<float*>(ring);  // [warp][head][kPad]
+#pragma unroll
+    for (int r = 0; r < kM; ++r) {
+      float top = s_m[0][g + 8 * r];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w][g + 8 * r]);
+      const float f = (top == minus_inf() ? 0.f : ex2(m[r] - top)) * (vref / kPScale);
+      float* const row = sums + (warp * S::kHeads + g + 8 * r) * S::kPad;
+#pragma unroll
+      for (int n = 0; n < S::kCols; n += 4) {
+        // columns 2c and 2c + 1 of blocks n .. n + 3 are codes of lanes 2c's and 2c + 1's eighths of the vector
+        constexpr int kCodes = 32 / kBits;  // of a word
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int d = word_byte<VP, 8>(n / kCodes, 2 * c + e) * 8 / kBits + n % kCodes;
+          float x[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k] = (kM == 1 ? o[n + k][e] + o[n + k][2 + e] : o[n + k][2 * r + e]) * f;
+          *reinterpret_cast<float4*>(row + d) = make_float4(x[0], x[1], x[2], x[3]);
+        }
+      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < heads * (kD / 4); i += kWarps * 32) {
+      const int h = i / (kD / 4), d = i % (kD / 4) * 4;
+      float top = s_m[0][h];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w][h]);
+      const float ref = top == minus_inf() ? 0.f : top;
+      float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+      float den = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 x = *reinterpret_cast<const float4*>(sums + (w * S::kHeads + h) * S::kPad + d);
+        num.x += x.x, num.y += x.y, num.z += x.z, num.w += x.w;
+        den += ex2(s_m[w][h] - ref) * s_l[w][h];
+      }
+      if (take < per_row) {  // part of a row: the one that begins it in the second place
+        const int64_t at = (blockIdx.x * 2 + (unit == 0 ? 1 : 0)) * S::kHeads + h;
+        *reinterpret_cast<float4*>(a.part + at * kD + d) = num;
+        if (d == 0) a.ml[at] = make_float2(top, den);
+      } else {
+        const float f = 1.f / den;
+        store_out4(a, b * a.o_batch + (h0 + h) * a.o_head + d, make_float4(num.x * f, num.y * f, num.z * f, num.w * f));
+        if (d == 0 && a.lse) a.lse[b * a.lse_batch + h0 + h] = kLn2 * (ref + log2f(den));
+      }
+    }
+    __syncthreads();  // before the next row's copies and operands
+  }
+}
+
+constexpr int kJoinWarps = 8;
+
+// Joins the parts of one row that several CTAs hold.  Few parts: a warp takes a head; many: all warps share a head's
+// parts.  A lane has four entries (and four more at 128).
+__global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const __grid_constant__ AttnArgs a, int heads_of_cta) {
+  __shared__ float s_num[kJoinWarps][256], s_den[kJoinWarps], s_top[kJoinWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.y;
+  const int D = a.c.head_dim;
+  const uint32_t row = blockIdx.x, rows = gridDim.x, per_row = units_of(a, __ldg(a.lens + b));
+  uint32_t before = 0, all = 0;  // units of the sequences before b, and of all
+  for (int i = lane; i < a.batch; i += 32) {
+    const uint32_t n = units_of(a, __ldg(a.lens + i));
+    all += n;
+    if (i < b) before += n;
+  }
+  before = __reduce_add_sync(0xffffffffu, before) * rows;
+  all = __reduce_add_sync(0xffffffffu, all) * rows;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // by every thread: this grid ends after k_attn's
+  if (per_row <= 1) return;
+  const Parts parts(all, min((uint32_t)a.ctas, all));
+  const uint32_t c0 = parts.cta_of(before + row * per_row), c1 = parts.cta_of(before + (row + 1) * per_row - 1);
+  if (c0 == c1) return;  // one CTA had the whole row and has written it
+  const int n = (int)(c1 - c0 + 1);
+  const int kv = row / a.head_chunks, h0 = kv * a.group + row % a.head_chunks * heads_of_cta;
+  const int heads = min(heads_of_cta, (kv + 1) * a.group - h0);
+
+  float top, den;
+  float4 num[2];
+  auto add = [&](int h, int s, int every) {
+    top = minus_inf(), den = 0.f;
+    num[0] = num[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (; s < n; s += every) {
+      const int64_t at = ((int64_t)(c0 + s) * 2 + (s == 0 ? 1 : 0)) * heads_of_cta + h;
+      const float2 ml = a.ml[at];
+      float4 x[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        x[k] = 4 * lane + 128 * k < D ? *reinterpret_cast<const float4*>(a.part + at * D + 4 * lane + 128 * k)
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float up = fmaxf(top, ml.x), ref = up == minus_inf() ? 0.f : up;
+      const float f = ex2(top - ref), g = ex2(ml.x - ref);
+      top = up;
+      den = den * f + g * ml.y;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        num[k].x = num[k].x * f + g * x[k].x, num[k].y = num[k].y * f + g * x[k].y;
+        num[k].z = num[k].z * f + g * x[k].z, num[k].w = num[k].w * f + g * x[k].w;
+      }
+    }
+  };
+  auto write_lse = [&](int h, float ref, float sum) {
+    if (a.lse) a.lse[b * a.lse_batch + h0 + h] = kLn2 * ((ref == minus_inf() ? 0.f : ref) + log2f(sum));
+  };
+  if (n <= 2 * kJoinWarps) {
+    for (int h = warp; h < heads; h += kJoinWarps) {
+      add(h, 0, 1);
+      const float f = 1.f / den;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (4 * lane + 128 * k < D)
+          store_out4(a, b * a.o_batch + (h0 + h) * a.o_head + 4 * lane + 128 * k,
+                     make_float4(num[k].x * f, num[k].y * f, num[k].z * f, num[k].w * f));
+      if (lane == 0) write_lse(h, top, den);
     }
     return;
   }
-
-  // ---- the query operands, shared by the warps: each warp prepares a part of the rows' scales first
-  for (int h = warp; h < S::kHeads; h += kWarps) {
-    uint32_t key = 0;
-    if (h < heads)
-      for (int d = lane; d < kD; d += 32) key = max(key, abs_key(load_q(a, b * a.q_batch + (h0 + h) * a.q_head + d)));
-    key = __reduce_max_sync(0xffffffffu, key);
-    if (lane == 0) s_mul[h] = __uint_as_float(key);
+  for (int h = 0; h < heads; ++h) {
+    add(h, warp, kJoinWarps);
+    if (lane == 0) s_den[warp] = den, s_top[warp] = top;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) *reinterpret_cast<float4*>(&s_num[warp][4 * lane + 128 * k]) = num[k];
+    __syncthreads();
+    top = s_top[0];
+    for (int w = 1; w < kJoinWarps; ++w) top = fmaxf(top, s_top[w]);
+    const float ref = top == minus_inf() ? 0.f : top;
+    const int d = threadIdx.x;
+    float sum = 0.f;
+    den = 0.f;
+    for (int w = 0; w < kJoinWarps; ++w) {
+      const float f = ex2(s_top[w] - ref);
+      sum += f * s_num[w][d];
+      den += f * s_den[w];
+    }
+    if (d < D) store_out(a, b * a.o_batch + (h0 + h) * a.o_head + d, sum / den);
+    if (d == 0) write_lse(h, top, den);
+    __syncthreads();
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < S::kSteps * 32 * kM; i += kWarps * 32) {
-    // entry (step, lane): with one operand {first part 0-1, second part 0-1, first 2-3, second 2-3} of head
-    // g; with two, the first (second) parts of heads g and g + 8 at entries 2 * step (+ 1)
-    const int l = i & 31, gg = l >> 2, cc = l & 3, st = (i >> 5) / kM, part = (i >> 5) % kM;
-    // four entries of the inner step: 8-bit codes are one word a step, 4-bit codes half a word
-    const int d = kBits == 8 ? word_byte<KP, 4>(st, cc) : 2 * word_byte<KP, 4>(st / 2, cc) + 4 * (st & 1);
-    uint32_t hi[kM][2], lo[kM][2];
-#pragma unroll
-    for (int r = 0; r < kM; ++r) {
-      const int h = gg + 8 * r;
-      float x[4] = {};
-      if (h < heads) {
-        const uint32_t key = __float_as_uint(s_mul[h]);
-        // 2^e with the largest entry in [2^14, 2^15); nothing for a non-finite row, whose scores become NaN
-        const int e = min(14 + 127 - (int)(key >> 23), 126);
-        const float up = key_finite(key) ? __uint_as_float((uint32_t)(e + 127) << 23) : 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float q = load_q(a, b * a.q_batch + (h0 + h) * a.q_head + d + j);
-          x[j] = up != 0.f ? q * up : 0.f;
-        }
-      }
-      split_f16(x[0], x[1], &hi[r][0], &lo[r][0]);
-      split_f16(x[2], x[3], &hi[r][1], &lo[r][1]);
-    }
-    if (kM == 1)
-      qs[i] = make_uint4(hi[0][0], lo[0][0], hi[0][1], lo[0][1]);
-    else
-      qs[i] = part == 0 ? make_uint4(hi[0][0], hi[kM - 1][0], hi[0][1], hi[kM - 1][1])
-                        : make_uint4(lo[0][0], lo[kM - 1][0], lo[0][1], lo[kM - 1][1]);
-  }
-  // the factor of a row's integer scores: scale * log2(e) / 2^e
-  float mul[kM];
-#pragma unroll
-  for (int r = 0; r < kM; ++r) {
-    const uint32_t key = __float_as_uint(s_mul[g + 8 * r]);
-    const int e = min(14 + 127 - (int)(key >> 23), 126);
-    mul[r] = key_finite(key) ? a.scale * kLog2e * __uint_as_float((uint32_t)(127 - e) << 23) : __uint_as_float(0x7FC00000u);
-  }
-  __syncthreads();
-
-  // ---- the warp's tiles
-  const int64_t first = begin + warp * kTile;
-  const int n_tiles = first < end ? (int)((end - first + kWarps * kTile - 1) / (kWarps * kTile)) : 0;
-  uint8_t* const mine = ring + warp * S::kRing;
-  const uint32_t mine_addr = smem_addr(mine);
-  const int32_t* const table = a.table + b * a.table_stride;
-  bool bad = false;
-  int32_t pages = 0;  // page of tile (i & ~31) + lane
-
-  auto issue = [&](int i) {
-    if (i < n_tiles) {
-      if ((i & 31) == 0) {
-        const int64_t t = first + (int64_t)(i + lane) * (kWarps * kTile);
-        pages = t < end ? table[t / a.c.page_size] : 0;
-        if (pages < 0 || pages >= a.c.n_pages) pages = -1;
-      }
-      const int32_t page = __shfl_sync(0xffffffffu, pages, i & 31);
-      bad |= page < 0;
-      const int64_t t0 = first + (int64_t)i * (kWarps * kTile);
-      const int in_page = (int)(t0 % a.c.page_size), valid = page < 0 ? 0 : (int)min((int64_t)kTile, end - t0);
-      const int64_t vec = kv * (int64_t)a.c.page_size + in_page, p = max(page, 0);
-      constexpr int kRow = kD * kBits / 8;
-      const uint8_t* kp = a.c.k + p * a.c.k_page_stride + vec * kRow;
-      const uint8_t* vp = a.c.v + p * a.c.v_page_stride + vec * kRow;
-      const uint32_t dst = mine_addr + (i % kStages) * S::kTileBytes;
-      // tokens that are not read keep the address of the tile's first one and are zero-filled
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int t = 8 * j + g, on = t < valid;
-        copy_pieces<KP, 4>(dst + j * (S::kKeyBytes / 2), lane, kp + (on ? t : 0) * kRow, c, on);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = 8 * (j >> 1) + 2 * c + (j & 1), on = t < valid;
-        copy_pieces<VP, 8>(dst + S::kKeyBytes + j * (S::kKeyBytes / 4), lane, vp + (on ? t : 0) * kRow, g, on);
-      }
-      if (lane < 8) {
-        const int n = min(max(valid - 2 * lane, 0), 2);
-        cp_async<16>(dst + 2 * S::kKeyBytes + lane * 16,
-                     a.c.steps + p * a.c.steps_page_stride + (vec + (n ? 2 * lane : 0)) * 2, 8u * n);
-      }
-    }
-    cp_async_commit();
-  };
-
-  float o[S::kCols][4] = {};
-  float m[kM], l[kM], vref = kStepFloor, winv = kPScale / kStepFloor;
-#pragma unroll
-  for (int r = 0; r < kM; ++r) m[r] = __uint_as_float(0xFF800000u), l[r] = 0.f;
-
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue(i);
-  for (int i = 0; i < n_tiles; ++i) {
-    cp_async_wait<kStages - 2>();
-    __syncwarp();
-    issue(i + kStages - 1);
-    const uint8_t* tile = mine + (i % kStages) * S::kTileBytes;
-    // scores: two blocks of eight tokens
-    float sc[2][4] = {};
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      uint32_t w[KP::kBytes / 4];
-      read_pieces<KP>(tile + j * (S::kKeyBytes / 2), lane, w);
-#pragma unroll
-      for (int st = 0; st < S::kSteps; ++st) {
-        uint32_t b0, b1;
-        if (kBits == 8) {
-          b0 = bytes_f16(w[st], 0x4140), b1 = bytes_f16(w[st], 0x4342);
-        } else {
-          const uint32_t x = (st & 1) ? w[st / 2] >> 8 : w[st / 2];
-          b0 = nibbles_f16<false>(x), b1 = nibbles_f16<true>(x);
-        }
-#pragma unroll
-        for (int r = 0; r < kM; ++r) {
-          const uint4 q = qs[(st * kM + r) * 32 + lane];
-          mma_f16(sc[j], q.x, q.y, q.z, q.w, b0, b1);
-        }
-      }
-    }
-    const float4 st0 = *reinterpret_cast<const float4*>(tile + 2 * S::kKeyBytes + c * 16);
-    const float4 st1 = *reinterpret_cast<const float4*>(tile + 2 * S::kKeyBytes + 64 + c * 16);
-    const float ks[4] = {st0.x, st0.z, st1.x, st1.z}, vs[4] = {st0.y, st0.w, st1.y, st1.w};
-    const int64_t left = end - (first + (int64_t)i * (kWarps * kTile));
-    // this lane's tokens 2c, 2c + 1, 2c + 8, 2c + 9; heads g (and g + 8)
-    float p[kM][4], fix[kM];
-    float vmax = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
-    vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
-    vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
-    float ratio = 1.f;
-    if (vmax > vref) {
-      ratio = vref / vmax;
-      vref = vmax;
-      winv = kPScale / vmax;
-    }
-    bool change = false;
-#pragma unroll
-    for (int r = 0; r < kM; ++r) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float dot = kM == 1 ? sc[j >> 1][j & 1] + sc[j >> 1][2 + (j & 1)] : sc[j >> 1][2 * r + (j & 1)];
-        p[r][j] = 8 * (j >> 1) + 2 * c + (j & 1) < left ? dot * ks[j] * mul[r] : __uint_as_float(0xFF800000u);
-      }
-      float top = fmaxf(fmaxf(p[r][0], p[r][1]), fmaxf(p[r][2], p[r][3]));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      top = fmaxf(top, m[r]);
-      const float ref = top == __uint_as_float(0xFF800000u) ? 0.f : top;
-      const float alpha = exp2f(m[r] - ref);
-      m[r] = top;
-      fix[r] = alpha * ratio;
-      change |= fix[r] != 1.f;
-      float sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        p[r][j] = exp2f(p[r][j] - ref);
-        sum += p[r][j];
-        p[r][j] *= vs[j] * winv;
-      }
-      l[r] = l[r] * alpha + sum;
-    }
-    if (__any_sync(0xffffffffu, change)) {
-#pragma unroll
-      for (int n = 0; n < S::kCols; ++n) {
-        o[n][0] *= fix[0], o[n][1] *= fix[0];
-        if (kM == 2) o[n][2] *= fix[kM - 1], o[n][3] *= fix[kM - 1];
-        else o[n][2] *= fix[0], o[n][3] *= fix[0];
-      }
-    }
-    // probabilities as operands
-    uint32_t hi[kM][2], lo[kM][2];
-#pragma unroll
-    for (int r = 0; r < kM; ++r) {
-      split_f16(p[r][0], p[r][1], &hi[r][0], &lo[r][0]);
-      split_f16(p[r][2], p[r][3], &hi[r][1], &lo[r][1]);
-    }
-    uint32_t w[4][VP::kBytes / 4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) read_pieces<VP>(tile + S::kKeyBytes + j * (S::kKeyBytes / 4), lane, w[j]);
-    auto product = [&](float (&acc)[4], uint32_t b0, uint32_t b1) {
-      if (kM == 1) {
-        mma_f16(acc, hi[0][0], lo[0][0], hi[0][1], lo[0][1], b0, b1);
-      } else {
-        mma_f16(acc, hi[0][0], hi[kM - 1][0], hi[0][1], hi[kM - 1][1], b0, b1);
-        mma_f16(acc, lo[0][0], lo[kM - 1][0], lo[0][1], lo[kM - 1][1], b0, b1);
-      }
-    };
-#pragma unroll
-    for (int n = 0; n < VP::kBytes / 4; ++n) {
-      if constexpr (kBits == 8) {
-        const uint32_t x0 = __byte_perm(w[0][n], w[1][n], 0x5140), x1 = __byte_perm(w[0][n], w[1][n], 0x7362);
-        const uint32_t y0 = __byte_perm(w[2][n], w[3][n], 0x5140), y1 = __byte_perm(w[2][n], w[3][n], 0x7362);
-        product(o[4 * n], bytes_f16(x0, 0x4140), bytes_f16(y0, 0x4140));
-        product(o[4 * n + 1], bytes_f16(x0, 0x4342), bytes_f16(y0, 0x4342));
-        product(o[4 * n + 2], bytes_f16(x1, 0x4140), bytes_f16(y1, 0x4140));
-        product(o[4 * n + 3], bytes_f16(x1, 0x4342), bytes_f16(y1, 0x4342));
-      } else {
-        // byte k of a word holds codes (0, 2), (4, 6), (1, 3), (5, 7) in its low and high half
-        constexpr int kSel[4] = {0x0400, 0x0501, 0x0602, 0x0703}, kLow[4] = {0, 4, 1, 5}, kUp[4] = {2, 6, 3, 7};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t x = __byte_perm(w[0][n], w[1][n], kSel[k]), y = __byte_perm(w[2][n], w[3][n], kSel[k]);
-          product(o[8 * n + kLow[k]], nibbles_f16<false>(x), nibbles_f16<false>(y));
-          product(o[8 * n + kUp[k]], nibbles_f16<true>(x), nibbles_f16<true>(y));
-        }
-      }
-    }
-  }
-  cp_async_wait<0>();
-
-  // ---- join the warps' sums
-#pragma unroll
-  for (int r = 0; r < kM; ++r) {
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-    if (__any_sync(0xffffffffu, bad)) l[r] = __uint_as_float(0x7FC00000u);
-    if (c == 0) s_m[warp][g + 8 * r] = m[r], s_l[warp][g + 8 * r] = l[r];
-  }
-  if (bad && lane == 0) set_status(a.status, IMQ_ERR_BOUNDS);
-  __syncthreads();  // the rings are done with: they hold the sums from here
-  float* const sums = reinterpret_cast<float*>(ring);  // [warp][head][kD + 4]
-  const float down = vref / kPScale;
-#pragma unroll
-  for (int n = 0; n < S::kCols; ++n) {
-    constexpr int kCodes = 32 / kBits;  // codes of a word
-    // column 2c (+ 1) of block n is code n of lane 2c's (2c + 1's) eighth of the vector
-    const int d0 = word_byte<VP, 8>(n / kCodes, 2 * c) * 8 / kBits + n % kCodes;
-    const int d1 = word_byte<VP, 8>(n / kCodes, 2 * c + 1) * 8 / kBits + n % kCodes;
-    float* row = sums + (warp * S::kHeads + g) * (kD + 4);
-    if (kM == 1) {
-      row[d0] = (o[n][0] + o[n][2]) * down, row[d1] = (o[n][1] + o[n][3]) * down;
-    } else {
-      row[d0] = o[n][0] * down, row[d1] = o[n][1] * down;
-      row += 8 * (kD + 4);
-      row[d0] = o[n][2] * down, row[d1] = o[n][3] * down;
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < heads * kD; i += kWarps * 32) {
-    const int h = i / kD, d = i % kD;
-    float top = s_m[0][h];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w][h]);
-    const float ref = top == __uint_as_float(0xFF800000u) ? 0.f : top;
-    float num = 0.f, den = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = exp2f(s_m[w][h] - ref);
-      num += f * sums[(w * S::kHeads + h) * (kD + 4) + d];
-      den += f * s_l[w][h];
-    }
-    if (a.splits > 1) {
-      const int64_t at = ((int64_t)b * a.splits + split) * q_heads + h0 + h;
-      a.part[at * kD + d] = num;
-      if (d == 0) a.ml[at] = make_float2(top, den);
-    } else {
-      store_out(a, b * a.o_batch + (h0 + h) * a.o_head + d, num / den);
-      if (d == 0 && a.lse) a.lse[b * a.lse_batch + h0 + h] = kLn2 * (ref + log2f(den));
-    }
-  }
-}
-
-// Joins the chunks of one sequence and query head: a thread per output entry.
-__global__ void k_attn_join(const __grid_constant__ AttnArgs a, int D) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int h = blockIdx.x, b = blockIdx.y, d = threadIdx.x, q_heads = gridDim.x;
-  const int64_t at = (int64_t)b * a.splits * q_heads + h;
-  float top = __uint_as_float(0xFF800000u);
-  for (int s = 0; s < a.splits; ++s) top = fmaxf(top, a.ml[at + (int64_t)s * q_heads].x);
-  const float ref = top == __uint_as_float(0xFF800000u) ? 0.f : top;
-  float num = 0.f, den = 0.f;
-  for (int s = 0; s < a.splits; ++s) {
-    const float2 ml = a.ml[at + (int64_t)s * q_heads];
-    if (ml.y == 0.f) continue;  // an empty chunk wrote no sums
-    const float f = exp2f(ml.x - ref);
-    num += f * a.part[(at + (int64_t)s * q_heads) * D + d];
-    den += f * ml.y;
-  }
-  // den = 0: no token at all
-  store_out(a, b * a.o_batch + h * a.o_head + d, den == 0.f ? 0.f : num / den);
-  if (d == 0 && a.lse) a.lse[b * a.lse_batch + h] = den == 0.f ? __uint_as_float(0xFF800000u) : kLn2 * (ref + log2f(den));
-}
-
-// Tokens of a split: chunks that fill the SMs once, none below 128 tokens.
-void plan_splits(int num_sms, int64_t batch, int64_t rows, int64_t limit, int64_t* chunk, int* splits) {
-  const int64_t ctas = batch * rows, want = 3ll * num_sms;
-  int64_t n = ctas > 0 ? want / ctas : 1;
-  if (n < 1) n = 1;
-  int64_t c = (limit + n - 1) / n;
-  c = (c + kWarps * kTile - 1) / (kWarps * kTile) * (kWarps * kTile);
-  if (c < 128) c = 128;
-  *chunk = c;
-  *splits = (int)(limit > 0 ? (limit + c - 1) / c : 1);
 }
 
 int heads_of_cta(int group) { return group > 8 ? 16 : 8; }
 
+// CTAs of k_attn: as many as the SMs hold at once (each takes an equal part of all the work), or a unit each.
+int64_t most_units(int64_t batch, int64_t rows, int64_t limit) { return batch * rows * ((limit + kUnit - 1) / kUnit); }
+bool has_parts(int64_t limit) { return limit > kUnit; }
+
 template <int kBits, int kD, int kM>
-imq_status launch_shape(const AttnArgs& a, dim3 grid, cudaStream_t st) {
+imq_status launch_shape(AttnArgs& a, int num_sms, int64_t rows, bool only_count, cudaStream_t st) {
   constexpr int kSmem = Shape<kBits, kD, kM>::kSmem;
   const void* fn = reinterpret_cast<const void*>(&k_attn<kBits, kD, kM>);
   if (ensure_smem(fn, kSmem) != cudaSuccess) return IMQ_ERR_CUDA;
-  k_attn<kBits, kD, kM><<<grid, kWarps * 32, kSmem, st>>>(a);
+  int per_sm = 0;
+  if (blocks_per_sm(fn, kWarps * 32, kSmem, &per_sm) != cudaSuccess || per_sm < 1) return IMQ_ERR_CUDA;
+  const int64_t most = most_units(a.batch, rows, a.limit);
+  a.ctas = (int)(most < 1 ? 1 : most < (int64_t)per_sm * num_sms ? most : (int64_t)per_sm * num_sms);
+  if (only_count) return IMQ_OK;
+  k_attn<kBits, kD, kM><<<a.ctas, kWarps * 32, kSmem, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? IMQ_OK : IMQ_ERR_CUDA;
 }
 
 template <int kBits, int kM>
-imq_status launch_dim(const AttnArgs& a, dim3 grid, cudaStream_t st) {
+imq_status launch_dim(AttnArgs& a, int num_sms, int64_t rows, bool only_count, cudaStream_t st) {
   switch (a.c.head_dim) {
-    case 64: return launch_shape<kBits, 64, kM>(a, grid, st);
-    case 128: return launch_shape<kBits, 128, kM>(a, grid, st);
-    case 192: return launch_shape<kBits, 192, kM>(a, grid, st);
-    default: return launch_shape<kBits, 256, kM>(a, grid, st);
+    case 64: return launch_shape<kBits, 64, kM>(a, num_sms, rows, only_count, st);
+    case 128: return launch_shape<kBits, 128, kM>(a, num_sms, rows, only_count, st);
+    case 192: return launch_shape<kBits, 192, kM>(a, num_sms, rows, only_count, st);
+    default: return launch_shape<kBits, 256, kM>(a, num_sms, rows, only_count, st);
   }
+}
+
+// Fills in a.ctas and, unless only that is asked for, launches k_attn.
+imq_status launch_main(AttnArgs& a, bool only_count, cudaStream_t st) {
+  DeviceState* ds;
+  const imq_status s = device_state(&ds);
+  if (s != IMQ_OK) return s;
+  a.status = ds->status;
+  const int64_t rows = (int64_t)a.head_chunks * a.c.n_heads;
+  const bool wide = heads_of_cta(a.group) == 16;
+  if (a.c.bits == 4)
+    return wide ? launch_dim<4, 2>(a, ds->num_sms, rows, only_count, st) : launch_dim<4, 1>(a, ds->num_sms, rows, only_count, st);
+  return wide ? launch_dim<8, 2>(a, ds->num_sms, rows, only_count, st) : launch_dim<8, 1>(a, ds->num_sms, rows, only_count, st);
+}
+
+size_t workspace_of(const AttnArgs& a) {
+  return has_parts(a.limit) ? (size_t)a.ctas * 2 * heads_of_cta(a.group) * ((size_t)a.c.head_dim * 4 + 8) : 0;
 }
 
 imq_status check_shape(const imq_kv_cache* c, int64_t batch, int32_t q_heads, int64_t max_len) {
   imq_status s = check_cache(c);
   if (s != IMQ_OK) return s;
   if (batch < 0 || q_heads < 1 || max_len < 0 || q_heads % c->n_heads != 0) return IMQ_ERR_ARG;
-  const int64_t group = q_heads / c->n_heads, per = heads_of_cta((int)group);
-  if (batch > 65535 || (group + per - 1) / per * c->n_heads > 65535 || q_heads > 65535 || max_len > INT32_MAX)
+  const int64_t group = q_heads / c->n_heads, per = heads_of_cta((int)group), rows = (group + per - 1) / per * c->n_heads;
+  if (batch > 65535 || q_heads > 65535 || max_len > (1 << 30) || most_units(batch, rows, max_len) > INT32_MAX)
     return IMQ_ERR_UNSUPPORTED;
   return IMQ_OK;
 }
@@ -514,15 +805,13 @@ imq_status paged_attention_workspace(const imq_kv_cache* c, int64_t batch, int32
   if (!bytes) return IMQ_ERR_ARG;
   imq_status s = check_shape(c, batch, q_heads, max_len);
   if (s != IMQ_OK) return s;
-  DeviceState* ds;
-  s = device_state(&ds);
-  if (s != IMQ_OK) return s;
-  const int group = q_heads / c->n_heads, per = heads_of_cta(group);
-  int64_t chunk;
-  int splits;
-  plan_splits(ds->num_sms, batch, (int64_t)((group + per - 1) / per) * c->n_heads, max_len, &chunk, &splits);
-  *bytes = splits > 1 ? (size_t)batch * splits * q_heads * ((size_t)c->head_dim * 4 + 8) : 0;
-  return IMQ_OK;
+  AttnArgs a = {};
+  a.c = *c, a.batch = (int)batch, a.limit = (int)max_len, a.group = q_heads / c->n_heads;
+  const int per = heads_of_cta(a.group);
+  a.head_chunks = (a.group + per - 1) / per;
+  s = launch_main(a, true, nullptr);
+  if (s == IMQ_OK) *bytes = workspace_of(a);
+  return s;
 }
 
 imq_status launch_paged_attention(const imq_kv_cache* c, const void* Q, imq_dtype qt, int64_t q_batch, int64_t q_head,
@@ -538,48 +827,43 @@ imq_status launch_paged_attention(const imq_kv_cache* c, const void* Q, imq_dtyp
     return IMQ_ERR_ARG;
   if (batch == 0) return IMQ_OK;
   if (!Q || !lens || !out || (table_width > 0 && !table)) return IMQ_ERR_ARG;
-  if ((reinterpret_cast<uintptr_t>(Q) & (qt == IMQ_F32 ? 3 : 1)) || (reinterpret_cast<uintptr_t>(out) & (ot == IMQ_F32 ? 3 : 1)) ||
-      (reinterpret_cast<uintptr_t>(lse) & 3) || (reinterpret_cast<uintptr_t>(workspace) & 15))
+  const uintptr_t qp = reinterpret_cast<uintptr_t>(Q);
+  if ((qp & (qt == IMQ_F32 ? 3 : 1)) || (reinterpret_cast<uintptr_t>(out) & (ot == IMQ_F32 ? 3 : 1)) ||
+      ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(lens) | reinterpret_cast<uintptr_t>(table)) & 3) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 15))
     return IMQ_ERR_ARG;
-  DeviceState* ds;
-  s = device_state(&ds);
-  if (s != IMQ_OK) return s;
-  AttnArgs a;
+  AttnArgs a = {};
   a.c = *c;
   a.Q = Q, a.q_batch = q_batch, a.q_head = q_head, a.q_bf16 = qt == IMQ_BF16;
+  const int64_t q_size = qt == IMQ_F32 ? 4 : 2;
+  a.q_vec = ((qp | (uintptr_t)(q_batch * q_size) | (uintptr_t)(q_head * q_size)) & (4 * q_size - 1)) == 0;
   a.group = q_heads / c->n_heads;
   const int per = heads_of_cta(a.group);
   a.head_chunks = (a.group + per - 1) / per;
-  a.table = table, a.table_stride = table_stride, a.lens = lens, a.limit = max_len;
-  plan_splits(ds->num_sms, batch, (int64_t)a.head_chunks * c->n_heads, max_len, &a.chunk, &a.splits);
+  a.table = table, a.table_stride = table_stride, a.lens = lens, a.batch = (int)batch, a.limit = (int)max_len;
   a.scale = scale;
   a.out = out, a.o_batch = o_batch, a.o_head = o_head, a.o_bf16 = ot == IMQ_BF16;
   a.lse = lse, a.lse_batch = lse_batch;
-  a.part = nullptr, a.ml = nullptr;
-  a.status = ds->status;
-  if (a.splits > 1) {
-    const size_t rows = (size_t)batch * a.splits * q_heads;
-    if (!workspace || workspace_bytes < rows * ((size_t)c->head_dim * 4 + 8)) return IMQ_ERR_BUFFER;
+  if (has_parts(max_len)) {
+    s = launch_main(a, true, st);
+    if (s != IMQ_OK) return s;
+    if (!workspace || workspace_bytes < workspace_of(a)) return IMQ_ERR_BUFFER;
     a.part = static_cast<float*>(workspace);
-    a.ml = reinterpret_cast<float2*>(a.part + rows * c->head_dim);
+    a.ml = reinterpret_cast<float2*>(a.part + (size_t)a.ctas * 2 * per * c->head_dim);
   }
-  const dim3 grid((unsigned)a.splits, (unsigned)(a.head_chunks * c->n_heads), (unsigned)batch);
-  if (c->bits == 4)
-    s = per == 8 ? launch_dim<4, 1>(a, grid, st) : launch_dim<4, 2>(a, grid, st);
-  else
-    s = per == 8 ? launch_dim<8, 1>(a, grid, st) : launch_dim<8, 2>(a, grid, st);
-  if (s != IMQ_OK || a.splits == 1) return s;
+  s = launch_main(a, false, st);
+  if (s != IMQ_OK || !has_parts(max_len)) return s;
   // launched before k_attn has finished; it waits for it on the device
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)q_heads, (unsigned)batch);
-  cfg.blockDim = dim3((unsigned)c->head_dim);
+  cfg.gridDim = dim3((unsigned)(a.head_chunks * c->n_heads), (unsigned)batch);
+  cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_attn_join, a, (int)c->head_dim) == cudaSuccess ? IMQ_OK : IMQ_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, k_attn_join, a, per) == cudaSuccess ? IMQ_OK : IMQ_ERR_CUDA;
 }
 
 }  // namespace imq

@@ -114,6 +114,16 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Signed by unsigned bytes, 32-bit integer sums: D = C + A (16 x 32) * B (32 x 8); a0 / b0 hold inner positions
+// 4c .. 4c + 3 and a2 / b1 16 + 4c .. + 3, a byte each; a1, a3 row g + 8.
+__device__ __forceinline__ void mma_s8u8(int32_t (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1, int32_t c0, int32_t c1, int32_t c2, int32_t c3) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.u8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(c0), "r"(c1), "r"(c2), "r"(c3));
+}
+
 // Codes as fp16 or bf16 pairs without integer-to-float conversions: a code's bits are set into the mantissa
 // of a power of two, where they count in units of one (or of 16), and the offset is subtracted; every step
 // is exact.

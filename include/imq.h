@@ -567,9 +567,9 @@ imq_status imq_paged_attention_workspace(const imq_kv_cache *cache, int64_t batc
  * 0 .. seq_lens[b] - 1 of sequence b, and the key head h / (n_q_heads / n_heads) of query head h:
  *   s_t = scale * sum_d Q[b, h, d] * key_t[d],  out[b, h, :] = sum_t softmax(s)_t * value_t,
  *   lse[b, h] = log sum_t exp(s_t)
- * Scores, softmax statistics and sums are fp32; codes enter the products exactly, queries with 22 bits
- * (and 2^-39 of the largest entry at the least), probabilities times the values' steps with 22 bits (and
- * 2^-40 of the largest at the least).  The order of the sums is fixed: equal inputs give equal bits.
+ * Scores, softmax statistics and sums are fp32.  Codes enter the products exactly; a query entry as an integer
+ * multiple of 2^-23 of its row's largest (a row below 1e-30 counts as zeros); a probability times its
+ * value's step with 22 bits, or to 2^-36 of the largest where that is more.  The order of the sums is fixed: equal inputs give equal bits.
  * Q           device, dtype qt (F32 or BF16): sequence b, head h at b * q_batch_stride + h * q_head_stride, head_dim
  *             consecutive entries.  A non-finite query gives NaN.
  * block_table device int32, batch rows of table_stride entries: entry j of a row is the page of tokens
@@ -584,7 +584,8 @@ imq_status imq_paged_attention_workspace(const imq_kv_cache *cache, int64_t batc
  * workspace   device, 16-byte aligned, at least imq_paged_attention_workspace bytes (IMQ_ERR_BUFFER otherwise); need
  *             not be initialised.  Calls whose executions overlap, and graphs that replay at the same time,
  *             need workspaces of their own.
- * n_q_heads must be a multiple of the cache's heads (IMQ_ERR_ARG).
+ * n_q_heads must be a multiple of the cache's heads (IMQ_ERR_ARG).  IMQ_ERR_UNSUPPORTED for a batch or a number of heads
+ * above 65535, max_len above 2^30, or batch * (cache heads) * max_len above about 2^37.
  */
 imq_status imq_paged_attention(const imq_kv_cache *cache, const void *Q, imq_dtype qt, int64_t q_batch_stride,
                                int64_t q_head_stride, int64_t batch, int32_t n_q_heads, const int32_t *block_table,

@@ -378,9 +378,9 @@ def plain_attention(cache, Q, table, lens, scale):
     A score is sum of D products, exact but for the query's 22 bits (2^-22 of its largest entry, each entry) and the
     roundings of D / 16 + 16 sums, then three more roundings: dx in all.  A weight exp(x - max) is off by two such
     errors and 2^-21 (the exponential, its argument's rounding), the value's part by 2^-21; the sums over the tokens
-    pass at most len / 64 + 60 roundings.  A weight times its step, in units of the largest step and of 2^-15, goes into
+    pass at most len / 64 + 60 roundings.  A weight times its step, in units of the largest step and of 2^-11, goes into
     two fp16 parts; the second is rounded to fp16's smallest spacing, 2^-24, where it is below 2^-14, so off by up to
-    2^-25 of those units whatever the weight: 2^-40 of the largest step, times a code of up to beta, per token.  (That
+    2^-25 of those units whatever the weight: 2^-36 of the largest step, times a code of up to beta, per token.  (That
     counts where a token that takes all the weight has a code of 0 and far smaller weights make the output.)"""
     k, v = cache_values(cache)
     B, Hq, D = Q.shape
@@ -405,7 +405,7 @@ def plain_attention(cache, Q, table, lens, scale):
             s = p.sum()
             out[b, h], lse[b, h] = p @ vv / s, top + np.log(s)
             rel = (n / 64 + 60) * U
-            floor = n * 2.0 ** -40 * (2 ** (cache.bits - 1) - 1) * steps[slot, h // G].max()
+            floor = n * 2.0 ** -36 * (2 ** (cache.bits - 1) - 1) * steps[slot, h // G].max()
             tol[b, h] = (floor + e @ np.abs(vv) + rel * (p @ np.abs(vv))) / s + (e.sum() / s + rel) * np.abs(out[b, h])
             ltol[b, h] = dx[x.argmax()] + e.sum() / s + rel + 4 * U * (1 + abs(lse[b, h]) + abs(top))
     return out, tol, lse, ltol
