@@ -570,21 +570,30 @@ def _float_dtype(dtype, what: str) -> int:
     return t
 
 
-def _on_device(*tensors):
-    """The calls launch on the current device: every tensor has to be there."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
-    for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
-            raise ValueError(f"expected a tensor on the current CUDA device, got one on {t.device}")
+def _device(first: torch.Tensor, *rest) -> int:
+    """The index of the device of all these tensors (None is none), which has to be the current one: the calls
+    launch there."""
+    dev = first.get_device()
+    for t in rest:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"expected all tensors on one device, got {first.device} and {t.device}")
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"expected tensors on the current CUDA device, got {first.device}")
+    return dev
 
 
-def _empty(shape, dtype, device, stream):
-    """A new tensor of the stream that will use it (so that its memory is not handed on too early)."""
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _empty(like: torch.Tensor, shape, dtype, stream):
+    """A new tensor on `like`'s device, of the stream that will use it (so that its memory is not handed on too
+    early)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape) if dtype is like.dtype else like.new_empty(shape, dtype=dtype)
     s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
     with torch.cuda.stream(s):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 class W4Weight:
@@ -614,16 +623,16 @@ def imq_w4_quantize(W: torch.Tensor, group: int = 128, transW: bool = False, cod
                     stream=None) -> W4Weight:
     """A float32 or bfloat16 weight, stored K x N (N x K when transW), in 4 bits."""
     wt = _float_dtype(W.dtype, "W")
-    _on_device(W, codes, steps)
+    dev = _device(W, codes, steps)
     ld = _ld(W)
     N, K = W.shape if transW else (W.shape[1], W.shape[0])
     if codes is None:
-        codes = _empty((N, W4Weight.row_bytes(K)), torch.uint8, W.device, stream)
+        codes = _empty(W, (N, W4Weight.row_bytes(K)), torch.uint8, stream)
     if steps is None:
-        steps = _empty((N, -(-K // int(group)) if int(group) > 0 else 0), torch.float32, W.device, stream)
+        steps = _empty(W, (N, -(-K // int(group)) if int(group) > 0 else 0), torch.float32, stream)
     w = W4Weight(codes, steps, K, N, group)
-    _check(lib().imq_w4_quantize(W.data_ptr(), wt, K, N, ld, int(transW), w.group, *w._args[:4], _stream(stream)),
-           "imq_w4_quantize")
+    _check(lib().imq_w4_quantize(W.data_ptr(), wt, K, N, ld, int(transW), w.group, *w._args[:4],
+                                 _raw_stream(stream, dev)), "imq_w4_quantize")
     return w
 
 
@@ -631,12 +640,12 @@ def imq_w4_dequantize(weight: W4Weight, dtype=torch.float32, transW: bool = Fals
     """The values of a 4-bit weight, K x N (N x K when transW)."""
     shape = (weight.N, weight.K) if transW else (weight.K, weight.N)
     if out is None:
-        out = _empty(shape, dtype, weight.codes.device, stream)
+        out = _empty(weight.codes, shape, dtype, stream)
     elif tuple(out.shape) != shape:
         raise ValueError(f"out must be {shape}")
     wt = _float_dtype(out.dtype, "out")
-    _on_device(weight.codes, out)
-    _check(lib().imq_w4_dequantize(*weight._args, out.data_ptr(), wt, _ld(out), int(transW), _stream(stream)),
+    dev = _device(weight.codes, out)
+    _check(lib().imq_w4_dequantize(*weight._args, out.data_ptr(), wt, _ld(out), int(transW), _raw_stream(stream, dev)),
            "imq_w4_dequantize")
     return out
 
@@ -644,16 +653,21 @@ def imq_w4_dequantize(weight: W4Weight, dtype=torch.float32, transW: bool = Fals
 def imq_w4_matvec(weight: W4Weight, X: torch.Tensor, out=None, out_dtype=None, stream=None) -> torch.Tensor:
     """X (M x K) times a 4-bit weight: M x N in out's dtype, out_dtype, or X's."""
     xt = _float_dtype(X.dtype, "X")
-    if X.dim() != 2 or X.size(1) != weight.K:
-        raise ValueError(f"X must be M x {weight.K}, not {tuple(X.shape)}")
-    M = X.size(0)
+    if X.dim() != 2 or X.size(1) != weight.K or (X.stride(1) != 1 and weight.K > 1):
+        raise ValueError(f"X must be M x {weight.K} with unit column stride, not {tuple(X.shape)}")
+    M, N = X.size(0), weight.N
     if out is None:
-        out = _empty((M, weight.N), X.dtype if out_dtype is None else out_dtype, X.device, stream)
-    elif tuple(out.shape) != (M, weight.N) or (out_dtype is not None and out.dtype != out_dtype):
-        raise ValueError(f"out must be {M} x {weight.N} of the output's dtype")
-    _on_device(weight.codes, X, out)
-    _check(lib().imq_w4_matvec(*weight._args, X.data_ptr(), xt, M, _ld(X), out.data_ptr(), _float_dtype(out.dtype, "out"),
-                               _ld(out), _stream(stream)), "imq_w4_matvec")
+        yt = xt if out_dtype is None else _float_dtype(out_dtype, "out")
+        out, ldy = _empty(X, (M, N), X.dtype if out_dtype is None else out_dtype, stream), N
+    else:
+        yt, ldy = _float_dtype(out.dtype, "out"), _ld(out)
+        if tuple(out.shape) != (M, N) or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError(f"out must be {M} x {N} of the output's dtype")
+    dev = _device(weight.codes, X, out)
+    st = lib().imq_w4_matvec(*weight._args, X.data_ptr(), xt, M, X.stride(0) if M > 1 else weight.K, out.data_ptr(), yt, ldy,
+                             _raw_stream(stream, dev))
+    if st:
+        _check(st, "imq_w4_matvec")
     return out
 
 
@@ -695,15 +709,15 @@ class KVCache:
 
 def _vectors(t, cache: KVCache, n: int, what: str):
     """(pointer, token stride, head stride) of (n, heads, head_dim) vectors."""
-    if tuple(t.shape) != (n, cache.n_heads, cache.head_dim) or t.stride(2) != 1:
+    if t.shape != (n, cache.n_heads, cache.head_dim) or t.stride(2) != 1:
         raise ValueError(f"{what} must be ({n}, {cache.n_heads}, {cache.head_dim}) with unit stride in the last axis")
     return t.data_ptr(), t.stride(0), t.stride(1)
 
 
 def _slots(slots) -> int:
-    if slots.dtype != torch.int64 or slots.dim() != 1 or (slots.numel() > 1 and slots.stride(0) != 1):
+    if slots.dtype != torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
         raise ValueError("slots must be a contiguous int64 vector")
-    return slots.numel()
+    return slots.size(0)
 
 
 def imq_kv_write(cache: KVCache, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, stream=None):
@@ -712,9 +726,11 @@ def imq_kv_write(cache: KVCache, K: torch.Tensor, V: torch.Tensor, slots: torch.
     if V.dtype != K.dtype:
         raise ValueError("K and V must have one dtype")
     n = _slots(slots)
-    _on_device(cache.k, K, V, slots)
-    _check(lib().imq_kv_write(cache._ref, *_vectors(K, cache, n, "K"), *_vectors(V, cache, n, "V"), xt, n, slots.data_ptr(),
-                              _stream(stream)), "imq_kv_write")
+    dev = _device(cache.k, K, V, slots)
+    st = lib().imq_kv_write(cache._ref, *_vectors(K, cache, n, "K"), *_vectors(V, cache, n, "V"), xt, n, slots.data_ptr(),
+                            _raw_stream(stream, dev))
+    if st:
+        _check(st, "imq_kv_write")
 
 
 def imq_kv_read(cache: KVCache, slots: torch.Tensor, dtype=torch.float32, K=None, V=None, stream=None):
@@ -723,28 +739,31 @@ def imq_kv_read(cache: KVCache, slots: torch.Tensor, dtype=torch.float32, K=None
     n = _slots(slots)
     shape = (n, cache.n_heads, cache.head_dim)
     if K is None:
-        K = _empty(shape, dtype if V is None else V.dtype, cache.k.device, stream)
+        K = _empty(cache.steps, shape, dtype if V is None else V.dtype, stream)
     if V is None:
-        V = _empty(shape, K.dtype, cache.k.device, stream)
+        V = _empty(K, shape, K.dtype, stream)
     yt = _float_dtype(K.dtype, "K")
     if V.dtype != K.dtype:
         raise ValueError("K and V must have one dtype")
-    _on_device(cache.k, slots, K, V)
-    _check(lib().imq_kv_read(cache._ref, slots.data_ptr(), n, *_vectors(K, cache, n, "K"), *_vectors(V, cache, n, "V"), yt,
-                             _stream(stream)), "imq_kv_read")
+    dev = _device(cache.k, slots, K, V)
+    st = lib().imq_kv_read(cache._ref, slots.data_ptr(), n, *_vectors(K, cache, n, "K"), *_vectors(V, cache, n, "V"), yt,
+                           _raw_stream(stream, dev))
+    if st:
+        _check(st, "imq_kv_read")
     return K, V
 
 
 def imq_paged_attention_workspace(cache: KVCache, batch: int, n_q_heads: int, max_len: int) -> int:
     """Workspace bytes of imq_paged_attention for these sizes."""
     key = (batch, n_q_heads, max_len)
-    if key not in cache._workspace:
+    need = cache._workspace.get(key)
+    if need is None:
         if len(cache._workspace) >= 64:  # lengths that grow step by step
             cache._workspace.clear()
         n = ctypes.c_size_t(0)
         _check(lib().imq_paged_attention_workspace(cache._ref, *key, ctypes.addressof(n)), "imq_paged_attention_workspace")
-        cache._workspace[key] = n.value
-    return cache._workspace[key]
+        need = cache._workspace[key] = n.value
+    return need
 
 
 def imq_paged_attention(cache: KVCache, Q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, max_len=None,
@@ -753,36 +772,44 @@ def imq_paged_attention(cache: KVCache, Q: torch.Tensor, block_table: torch.Tens
     (out, lse), lse None unless wanted.  block_table int32 (batch, pages of the longest), seq_lens int32 (batch).
     max_len bounds seq_lens (default: what the table covers); scale defaults to head_dim ** -0.5."""
     qt = _float_dtype(Q.dtype, "Q")
-    if Q.dim() != 3 or Q.size(2) != cache.head_dim or Q.stride(2) != 1:
-        raise ValueError(f"Q must be (batch, query heads, {cache.head_dim}) with unit stride in the last axis")
-    batch, heads, _ = Q.shape
+    D = cache.head_dim
+    if Q.dim() != 3 or Q.size(2) != D or Q.stride(2) != 1:
+        raise ValueError(f"Q must be (batch, query heads, {D}) with unit stride in the last axis")
+    batch, heads, _ = shape = Q.shape
     if heads == 0 or heads % cache.n_heads:
         raise ValueError(f"{heads} query heads on {cache.n_heads} key heads")
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.size(0) != batch or (
             block_table.size(1) > 1 and block_table.stride(1) != 1):
         raise ValueError("block_table must be int32 (batch, pages) with unit stride in the last axis")
-    if seq_lens.dtype != torch.int32 or tuple(seq_lens.shape) != (batch,) or (batch > 1 and seq_lens.stride(0) != 1):
+    if seq_lens.dtype != torch.int32 or seq_lens.shape != (batch,) or not seq_lens.is_contiguous():
         raise ValueError("seq_lens must be a contiguous int32 vector of the batch")
     width = block_table.size(1)
     max_len = width * cache.page_size if max_len is None else int(max_len)
     if out is None:
-        out = _empty((batch, heads, cache.head_dim), Q.dtype if out_dtype is None else out_dtype, Q.device, stream)
-    elif out.shape != Q.shape or out.stride(2) != 1 or (out_dtype is not None and out.dtype != out_dtype):
-        raise ValueError("out must have Q's shape, unit stride in the last axis and the output's dtype")
-    ot = _float_dtype(out.dtype, "out")
+        ot = qt if out_dtype is None else _float_dtype(out_dtype, "out")
+        out = _empty(Q, shape, Q.dtype if out_dtype is None else out_dtype, stream)
+    else:
+        ot = _float_dtype(out.dtype, "out")
+        if out.shape != shape or out.stride(2) != 1 or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError("out must have Q's shape, unit stride in the last axis and the output's dtype")
     if lse is None:
         if want_lse:
-            lse = _empty((batch, heads), torch.float32, Q.device, stream)
-    elif lse.dtype != torch.float32 or tuple(lse.shape) != (batch, heads) or (heads > 1 and lse.stride(1) != 1):
+            lse = _empty(cache.steps, (batch, heads), torch.float32, stream)
+    elif lse.dtype != torch.float32 or lse.shape != (batch, heads) or (heads > 1 and lse.stride(1) != 1):
         raise ValueError("lse must be float32 (batch, query heads) with unit stride in the last axis")
+    dev = _device(cache.k, Q, block_table, seq_lens, out, lse, workspace)
     need = imq_paged_attention_workspace(cache, batch, heads, max_len)
-    if workspace is None and need:
-        workspace = _empty(need, torch.uint8, Q.device, stream)
-    _on_device(cache.k, Q, block_table, seq_lens, out, lse, workspace)
-    _check(lib().imq_paged_attention(
+    if workspace is None:
+        room = need
+        if need:
+            workspace = _empty(cache.k, (need,), torch.uint8, stream)
+    else:
+        room = workspace.numel() * workspace.element_size()
+    st = lib().imq_paged_attention(
         cache._ref, Q.data_ptr(), qt, Q.stride(0), Q.stride(1), batch, heads, block_table.data_ptr(), block_table.stride(0),
-        width, seq_lens.data_ptr(), max_len, cache.head_dim ** -0.5 if scale is None else float(scale), out.data_ptr(), ot,
-        out.stride(0), out.stride(1), None if lse is None else lse.data_ptr(), 0 if lse is None else lse.stride(0),
-        None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)), "imq_paged_attention")
+        width, seq_lens.data_ptr(), max_len, D ** -0.5 if scale is None else scale, out.data_ptr(), ot, out.stride(0),
+        out.stride(1), None if lse is None else lse.data_ptr(), 0 if lse is None else lse.stride(0),
+        None if workspace is None else workspace.data_ptr(), room, _raw_stream(stream, dev))
+    if st:
+        _check(st, "imq_paged_attention")
     return out, lse

@@ -18,18 +18,20 @@
 //   - p * v runs on fp16 with fp32 sums: codes are exact in fp16; a probability times its value's step, in units
 //     of the largest step so far and of 2^-11, is cut into two fp16 parts, 22 bits together.  With up to 8
 //     query heads both parts share one 16-row operand, so the second costs no further instruction.
-// The inner axis of a product may be permuted at will if both operands agree, so a lane's 16 (8, 4) bytes
-// of a key are contiguous ones, and a lane's bytes of four values make the columns of the second product.
+// The inner axis of a product may be permuted at will if both operands agree, so a lane's 16 (or 8) bytes of a
+// key are contiguous ones.  Values are transposed on the way from shared memory (pairs of bytes, or four
+// nibbles, of two tokens to a register), and the columns they make are sorted out when the sums are written.
 //
 // The softmax keeps a reference instead of the running maximum: it is raised (and the sums rescaled) only when a
-// score exceeds it by 4 (a weight 16, the room that fp16 leaves above 2^11), so most tiles need no exchange
-// between lanes.
+// weight exceeds it 8 times, or a value's step the unit of steps twice (together the room that fp16 leaves above
+// 2^11), so most tiles need no exchange between lanes.
 //
 // Split: the work of all sequences and key heads lies in one line of units of 64 tokens, cut into equal parts, one
 // for each CTA that the SMs hold at once; so lengths may differ as they will.  A CTA's four warps take tiles
 // of 16 tokens in turn, each with its own ring of asynchronous copies (every lane copies what it will use
 // itself, so a tile waits for no barrier but the warp's), and join in shared memory.  Rows that several CTAs
 // share join in k_attn_join from partial sums in the workspace, in a fixed order.
+#include <atomic>
 #include <type_traits>
 
 #include "lowbit.cuh"
@@ -42,7 +44,8 @@ constexpr int kWarps = 4;
 constexpr int kTile = 16;              // tokens of a warp's tile; it lies in one page (pages are multiples of it)
 constexpr int kUnit = kWarps * kTile;  // tokens: the grain of the split
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 4.f;          // how far, in powers of two, a weight may exceed the reference's
+constexpr float kSlack = 3.f;          // how far, in powers of two, a weight may exceed the reference's,
+constexpr float kStepSlack = 2.f;      // and how many times a step the unit of steps
 constexpr float kPScale = 2048.f;      // unit of the weights in fp16: 2^15 is the largest
 constexpr float kStepFloor = 1e-30f;   // the unit of the steps starts here
 constexpr float kQMax = 8355711.f;     // 127 * 65536 + 127 * 256 + 127
@@ -71,25 +74,19 @@ struct AttnArgs {
   int32_t* status;
 };
 
-// Bytes a lane holds of a token's key (a quarter of the vector) and of a value (an eighth), as 16-, 8- and
-// 4-byte pieces.  Piece p of the lanes of a token together is a contiguous part of the vector.
-template <int kBits, int kD, int kShare>
+// Bytes a lane holds of a token's key (a quarter of the vector), as 16-byte pieces and an 8-byte one.  Piece p of the
+// four lanes of a token together is a contiguous part of the vector; in shared memory a piece of a warp is 32
+// consecutive slots.
+template <int kBits, int kD>
 struct Pieces {
-  static constexpr int kBytes = kD * kBits / 8 / kShare;
-  static constexpr int n16 = kBytes / 16, n8 = kBytes % 16 / 8, n4 = kBytes % 8 / 4;
+  static constexpr int kBytes = kD * kBits / 32, n16 = kBytes / 16, n8 = kBytes % 16 / 8;
+  // entry d of a vector (d a multiple of 4): the lane column that holds it and its word among the lane's
+  static __device__ __forceinline__ void find(int d, int* column, int* word) {
+    const int at = d * kBits / 8;
+    if (at < n16 * 64) *column = at % 64 / 16, *word = at / 64 * 4 + at % 16 / 4;
+    else *column = (at - n16 * 64) / 8, *word = n16 * 4 + (at - n16 * 64) % 8 / 4;
+  }
 };
-
-// Copies lane `i` of kShare lanes' pieces of the vector at src to dst, laid out so that each piece of a warp
-// is 32 consecutive slots; `on` false writes zeros and reads nothing.
-template <typename P, int kShare>
-__device__ __forceinline__ void copy_pieces(uint32_t dst, int lane, const uint8_t* src, int i, bool on) {
-#pragma unroll
-  for (int j = 0; j < P::n16; ++j) cp_async<16>(dst + (j * 32 + lane) * 16, src + (j * kShare + i) * 16, on ? 16u : 0u);
-  if (P::n8) cp_async<8>(dst + P::n16 * 512 + lane * 8, src + P::n16 * kShare * 16 + i * 8, on ? 8u : 0u);
-  if (P::n4)
-    cp_async<4>(dst + P::n16 * 512 + P::n8 * 256 + lane * 4, src + P::n16 * kShare * 16 + P::n8 * kShare * 8 + i * 4, on ? 4u : 0u);
-}
-// The lane's words of those pieces.
 template <typename P>
 __device__ __forceinline__ void read_pieces(const uint8_t* src, int lane, uint32_t (&w)[P::kBytes / 4]) {
 #pragma unroll
@@ -101,17 +98,6 @@ __device__ __forceinline__ void read_pieces(const uint8_t* src, int lane, uint32
     const uint2 v = *reinterpret_cast<const uint2*>(src + P::n16 * 512 + lane * 8);
     w[4 * P::n16] = v.x, w[4 * P::n16 + 1] = v.y;
   }
-  if (P::n4) w[4 * P::n16 + 2 * P::n8] = *reinterpret_cast<const uint32_t*>(src + P::n16 * 512 + P::n8 * 256 + lane * 4);
-}
-// Byte of the vector at which word i of lane `l` of kShare lanes lies.
-template <typename P, int kShare>
-__device__ __forceinline__ int word_byte(int i, int l) {
-  if (i < 4 * P::n16) return (i / 4 * kShare + l) * 16 + i % 4 * 4;
-  i -= 4 * P::n16;
-  int base = P::n16 * kShare * 16;
-  if (i < 2 * P::n8) return base + l * 8 + i * 4;
-  base += P::n8 * kShare * 8;
-  return base + l * 4;
 }
 
 // Four consecutive entries; vec: they are aligned to their size together.
@@ -180,12 +166,20 @@ struct Parts {
 // kM: 1 for up to 8 query heads a key head, 2 for 9 to 16.
 template <int kBits, int kD, int kM>
 struct Shape {
-  using KP = Pieces<kBits, kD, 4>;
-  using VP = Pieces<kBits, kD, 8>;
-  static constexpr int kRow = kD * kBits / 8;
+  using KP = Pieces<kBits, kD>;
+  static constexpr int kRow = kD * kBits / 8, kChunks = kRow / 16;
+  // Values lie in rows of 16-byte chunks; eight rows' chunks of one column are in different banks: by an exclusive or
+  // of the chunk with the row where a row is a power of two, by a chunk of padding where it is not.
+  static constexpr bool kPadded = (kRow & (kRow - 1)) != 0;
+  static constexpr int kPitch = kRow + (kPadded ? 16 : 0);
+  static __device__ __forceinline__ int chunk_at(int row, int chunk) {
+    const int mix = kPadded ? 0 : kRow >= 128 ? row & 7 : kRow == 64 ? (row >> 1) & 3 : (row >> 2) & 1;
+    return row * kPitch + (chunk ^ mix) * 16;
+  }
   static constexpr int kSteps = kD / 32;               // inner steps of q * k
   static constexpr int kCols = kD / 8;                 // 8-column blocks of p * v
-  static constexpr int kTileBytes = 32 * kRow + 128;   // keys, values, steps of 16 tokens
+  static constexpr int kValues = 16 * kRow, kStepsAt = kValues + 16 * kPitch;
+  static constexpr int kTileBytes = kStepsAt + 128;    // keys, values, steps of 16 tokens
   // about 13 KB for a warp's ring: 16 warps an SM have 130 KB of copies under way
   static constexpr int kStages = 13000 / kTileBytes < 2 ? 2 : 13000 / kTileBytes > 8 ? 8 : 13000 / kTileBytes;
   static constexpr int kRing = kStages * kTileBytes;
@@ -208,12 +202,12 @@ __device__ __forceinline__ void prepare_query(uint4* qs, int32_t (*s_dig)[8 * kM
   uint8_t* const bytes = reinterpret_cast<uint8_t*>(qs);
   // a warp takes a head: lane i its entries 4i .. 4i + 3 (and 128 further on)
   constexpr int kParts = (kD + 127) / 128;
-  for (int h = warp; h < 8 * kM; h += kWarps) {
+  for (int h = warp; h < heads; h += kWarps) {
     float x[kParts][4] = {};
     uint32_t key = 0;
 #pragma unroll
     for (int p = 0; p < kParts; ++p)
-      if (h < heads && 4 * lane + 128 * p < kD) {
+      if (4 * lane + 128 * p < kD) {
         load(h, 4 * lane + 128 * p, x[p]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) key = max(key, abs_key(x[p][j]));
@@ -249,20 +243,14 @@ __device__ __forceinline__ void prepare_query(uint4* qs, int32_t (*s_dig)[8 * kM
         // kM = 1: operand 0 holds the first digit in row g and the second in row g + 8, operand 1 the third in row g;
         // kM = 2: an operand a digit, heads g and g + 8
         const int op = kM == 1 ? k / 2 : k, high = kM == 1 ? k % 2 : h / 8, g = kM == 1 ? h : h % 8;
+        int c, w;
+        S::KP::find(d, &c, &w);
         if constexpr (kBits == 8) {
-          // four entries are one word of a key: word w of column c; inner step w / 2, first or second four
-          const int at = d;
-          int c, w;
-          if (at < S::KP::n16 * 64) c = at % 64 / 16, w = at / 64 * 4 + at % 16 / 4;
-          else c = (at - S::KP::n16 * 64) / 8, w = S::KP::n16 * 4 + (at - S::KP::n16 * 64) % 8 / 4;
+          // four entries are one word of a key: inner step w / 2, its first or second four positions
           reinterpret_cast<uint32_t*>(bytes)[((w / 2 * S::kQOps + op) * 32 + g * 4 + c) * 4 + (w % 2) * 2 + high] = dig[k];
         } else {
           // a word of a key is eight entries, its even nibbles (codes 0, 4, 1, 5) the first four positions of the
           // step and its odd ones (codes 2, 6, 3, 7) the second; these four entries are codes 0-3 or 4-7
-          const int at = d / 2;  // byte of the vector (a multiple of 2)
-          int c, w;
-          if (at < S::KP::n16 * 64) c = at % 64 / 16, w = at / 64 * 4 + at % 16 / 4;
-          else c = (at - S::KP::n16 * 64) / 8, w = S::KP::n16 * 4 + (at - S::KP::n16 * 64) % 8 / 4;
           const int e = d % 8 / 4;
           uint8_t* const to = bytes + (((w * S::kQOps + op) * 32 + g * 4 + c) * 4 + high) * 4;
           to[e] = dig[k] & 255, to[e + 2] = dig[k] >> 8 & 255;            // codes 0 and 1 (4 and 5)
@@ -273,7 +261,11 @@ __device__ __forceinline__ void prepare_query(uint4* qs, int32_t (*s_dig)[8 * kM
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
       sum[k] = __reduce_add_sync(0xffffffffu, sum[k]);
-      if (lane == 0) s_dig[k][h] = -(1 << (kBits - 1)) * sum[k];
+    }
+    // the offset of the stored codes times a row's digits: of the first two digits together, and of the third
+    if (lane == 0) {
+      s_dig[0][h] = -(1 << (kBits - 1)) * (256 * sum[0] + sum[1]);
+      s_dig[1][h] = -(1 << (kBits - 1)) * sum[2];
     }
   }
 }
@@ -282,20 +274,20 @@ template <int kBits, int kD, int kM>
 __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_attn(const __grid_constant__ AttnArgs a) {
   using S = Shape<kBits, kD, kM>;
   using KP = typename S::KP;
-  using VP = typename S::VP;
   constexpr int kStages = S::kStages, kRow = S::kRow;
   extern __shared__ __align__(16) uint8_t smem[];
   uint4* const qs = reinterpret_cast<uint4*>(smem);
   uint8_t* const ring = smem + S::kQBytes;
   __shared__ float s_mul[S::kHeads];
-  __shared__ int32_t s_dig[3][S::kHeads];
+  __shared__ int32_t s_dig[2][S::kHeads];
   __shared__ float s_m[kWarps][S::kHeads], s_l[kWarps][S::kHeads];
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   const uint32_t rows = a.c.n_heads * a.head_chunks;
   asm volatile("griddepcontrol.launch_dependents;");
-  // the last rows of the operands that hold no digit stay zero
+  // rows of the operands that hold no head's digit stay zero (or as an earlier row of this CTA left them)
   for (int i = threadIdx.x; i < S::kQBytes / 16; i += kWarps * 32) qs[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (threadIdx.x < S::kHeads) s_mul[threadIdx.x] = 0.f, s_dig[0][threadIdx.x] = s_dig[1][threadIdx.x] = 0;
 
   // ---- this CTA's part of the line: units u0 .. u1 - 1 (every warp finds it by itself)
   uint32_t all = 0;
@@ -375,9 +367,9 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
 
     // ---- the warp's copies
     const uint32_t mine = smem_addr(ring) + warp * S::kRing;
-    const uint8_t* const k_base = a.c.k + (int64_t)kv * a.c.page_size * kRow;
-    const uint8_t* const v_base = a.c.v + (int64_t)kv * a.c.page_size * kRow;
-    const float* const s_base = a.c.steps + (int64_t)kv * a.c.page_size * 2;
+    const uint8_t* const k_base = a.c.k + (int64_t)kv * a.c.page_size * kRow + g * kRow + c * 16;
+    const uint8_t* const v_base = a.c.v + (int64_t)kv * a.c.page_size * kRow + lane * 16;
+    const float* const s_base = a.c.steps + (int64_t)kv * a.c.page_size * 2 + lane * 4;
     bool bad = false;
     uint32_t fill = mine;  // the stage that is filled next
     auto issue = [&](int i) {
@@ -389,18 +381,25 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
         const int32_t page = __shfl_sync(0xffffffffu, page_now, i & 31);
         const uint32_t place = __shfl_sync(0xffffffffu, place_now, i & 31);
         const int left = end - (first + i * kUnit);
-        const uint64_t p = max(page, 0);
-        const uint8_t* kp = k_base + p * (uint64_t)a.c.k_page_stride + place * (uint32_t)kRow;
-        const uint8_t* vp = v_base + p * (uint64_t)a.c.v_page_stride + place * (uint32_t)kRow;
-        const float* sp = s_base + p * (uint64_t)a.c.steps_page_stride + place * 2u;
+        const uint64_t p = (uint32_t)max(page, 0);
+        const uint8_t* kp = k_base + p * (uint32_t)a.c.k_page_stride + (uint64_t)place * (uint32_t)kRow;
+        const uint8_t* vp = v_base + p * (uint32_t)a.c.v_page_stride + (uint64_t)place * (uint32_t)kRow;
+        const float* sp = s_base + p * (uint32_t)a.c.steps_page_stride + (uint64_t)place * 2u;
+        const uint32_t to16 = fill + lane * 16, to8 = fill + lane * 8 + KP::n16 * 512;
         if (left >= kTile && page >= 0) {
-          kp += g * kRow, vp += 2 * c * kRow;
+          // keys: tokens g and g + 8, this lane's quarter; values: the tile's bytes in order
 #pragma unroll
-          for (int j = 0; j < 2; ++j) copy_pieces<KP, 4>(fill + j * 8 * kRow, lane, kp + 8 * j * kRow, c, true);
+          for (int j = 0; j < 2; ++j) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            copy_pieces<VP, 8>(fill + (16 + 4 * j) * kRow, lane, vp + (8 * (j >> 1) + (j & 1)) * kRow, g, true);
-          if (lane < 8) cp_async<16>(fill + 32 * kRow + lane * 16, sp + lane * 4, 16u);
+            for (int q = 0; q < KP::n16; ++q) cp_async<16>(to16 + j * 8 * kRow + q * 512, kp + j * 8 * kRow + q * 64);
+            if (KP::n8) cp_async<8>(to8 + j * 8 * kRow, kp - 8 * c + j * 8 * kRow + 64 * KP::n16);
+          }
+#pragma unroll
+          for (int q = 0; q < S::kChunks / 2; ++q) {
+            const int at = q * 32 + lane;
+            cp_async<16>(fill + S::kValues + S::chunk_at(at / S::kChunks, at % S::kChunks), vp + q * 512);
+          }
+          if (lane < 8) cp_async<16>(to16 + S::kStepsAt, sp);
         } else {
           // the end of the sequence, or a page outside the cache: what is not read is zero-filled (steps of 0: no
           // stale value meets a weight of 0), with an address that is not read either
@@ -408,16 +407,20 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
           bad |= page < 0;
 #pragma unroll 1
           for (int j = 0; j < 2; ++j) {
-            const int t = 8 * j + g;
-            copy_pieces<KP, 4>(fill + j * 8 * kRow, lane, kp + (t < valid ? t : 0) * kRow, c, t < valid);
+            const bool on = 8 * j + g < valid;
+            const uint8_t* from = on ? kp + j * 8 * kRow : a.c.k;
+#pragma unroll
+            for (int q = 0; q < KP::n16; ++q) cp_async_part<16>(to16 + j * 8 * kRow + q * 512, from + (on ? q * 64 : 0), on ? 16u : 0u);
+            if (KP::n8) cp_async_part<8>(to8 + j * 8 * kRow, from + (on ? 64 * KP::n16 - 8 * c : 0), on ? 8u : 0u);
           }
 #pragma unroll 1
-          for (int j = 0; j < 4; ++j) {
-            const int t = 8 * (j >> 1) + 2 * c + (j & 1);
-            copy_pieces<VP, 8>(fill + (16 + 4 * j) * kRow, lane, vp + (t < valid ? t : 0) * kRow, g, t < valid);
+          for (int q = 0; q < S::kChunks / 2; ++q) {
+            const int at = q * 32 + lane;
+            const bool on = at / S::kChunks < valid;
+            cp_async_part<16>(fill + S::kValues + S::chunk_at(at / S::kChunks, at % S::kChunks), on ? vp + q * 512 : a.c.v, on ? 16u : 0u);
           }
           const int n = min(max(valid - 2 * lane, 0), 2);
-          if (lane < 8) cp_async<16>(fill + 32 * kRow + lane * 16, sp + (n ? lane * 4 : 0), 8u * n);
+          if (lane < 8) cp_async_part<16>(to16 + S::kStepsAt, n ? sp : a.c.steps, 8u * n);
         }
         fill = fill + S::kTileBytes == mine + S::kRing ? mine : fill + S::kTileBytes;
       }
@@ -441,12 +444,12 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
     }
     __syncthreads();
     float mul[kM];
-    int32_t start[3][kM];  // what the digits' sums start from
+    int32_t start[2][kM];  // the offset's part of the first two digits' sums together, and of the third's
 #pragma unroll
     for (int r = 0; r < kM; ++r) {
       mul[r] = s_mul[g + 8 * r];
 #pragma unroll
-      for (int k = 0; k < 3; ++k) start[k][r] = s_dig[k][g + 8 * r];
+      for (int k = 0; k < 2; ++k) start[k][r] = s_dig[k][g + 8 * r];
     }
 
     // ---- the warp's tiles
@@ -465,7 +468,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
       // (and g + 8)
       float p[kM][4];
       {
-        int32_t acc[2][S::kQOps][4];
+        int32_t acc[2][S::kQOps][4] = {};
         uint32_t w[2][KP::kBytes / 4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) read_pieces<KP>(tile + j * 8 * kRow, lane, w[j]);
@@ -478,14 +481,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
             for (int j = 0; j < 2; ++j) {
               const uint32_t b0 = kBits == 8 ? w[j][kBits == 8 ? 2 * st : 0] : w[j][kBits == 8 ? 0 : st] & 0x0F0F0F0Fu;
               const uint32_t b1 = kBits == 8 ? w[j][kBits == 8 ? 2 * st + 1 : 0] : w[j][kBits == 8 ? 0 : st] >> 4 & 0x0F0F0F0Fu;
-              int32_t(&d)[4] = acc[j][op];
-              if (st == 0) {
-                const int32_t c0 = kM == 1 ? (op == 0 ? start[0][0] : start[2][0]) : start[op][0];
-                const int32_t c2 = kM == 1 ? (op == 0 ? start[1][0] : 0) : start[op][kM - 1];
-                mma_s8u8(d, q.x, q.y, q.z, q.w, b0, b1, c0, c0, c2, c2);
-              } else {
-                mma_s8u8(d, q.x, q.y, q.z, q.w, b0, b1, d[0], d[1], d[2], d[3]);
-              }
+              mma_s8u8(acc[j][op], q.x, q.y, q.z, q.w, b0, b1);
             }
           }
         }
@@ -497,14 +493,14 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
             const int32_t d0 = kM == 1 ? x[0][j & 1] : x[0][2 * r + (j & 1)];
             const int32_t d1 = kM == 1 ? x[0][2 + (j & 1)] : x[kM - 1][2 * r + (j & 1)];
             const int32_t d2 = kM == 1 ? x[1][j & 1] : x[kM][2 * r + (j & 1)];
-            p[r][j] = fmaf((float)(d0 * 256 + d1), 256.f, (float)d2);
+            p[r][j] = fmaf((float)(d0 * 256 + d1 + start[0][r]), 256.f, (float)(d2 + start[1][r]));
           }
       }
-      const float4 st0 = *reinterpret_cast<const float4*>(tile + 32 * kRow + c * 16);
-      const float4 st1 = *reinterpret_cast<const float4*>(tile + 32 * kRow + 64 + c * 16);
+      const float4 st0 = *reinterpret_cast<const float4*>(tile + S::kStepsAt + c * 16);
+      const float4 st1 = *reinterpret_cast<const float4*>(tile + S::kStepsAt + 64 + c * 16);
       const float ks[4] = {st0.x, st0.z, st1.x, st1.z}, vs[4] = {st0.y, st0.w, st1.y, st1.w};
       const int left = end - (first + i * kUnit);
-      bool raise = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3])) > vref;
+      bool raise = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3])) > kStepSlack * vref;
 #pragma unroll
       for (int r = 0; r < kM; ++r)
 #pragma unroll
@@ -565,26 +561,22 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
           mma_f16(acc, lo[0][0], lo[kM - 1][0], lo[0][1], lo[kM - 1][1], b0, b1);
         }
       };
-      uint32_t w[4][VP::kBytes / 4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) read_pieces<VP>(tile + (16 + 4 * j) * kRow, lane, w[j]);
+      for (int q = 0; q < S::kChunks; q += 2) {
+        // chunks q and q + 1 of tokens 0-7 and 8-15; a register holds two bytes (four nibbles) of tokens 2c and 2c + 1
+        uint32_t w[4];
+        ldmatrix_trans4(smem_addr(tile) + S::kValues + S::chunk_at(lane % 16, q + lane / 16), w);
 #pragma unroll
-      for (int n = 0; n < VP::kBytes / 4; ++n) {
-        if constexpr (kBits == 8) {
-          const uint32_t x0 = __byte_perm(w[0][n], w[1][n], 0x5140), x1 = __byte_perm(w[0][n], w[1][n], 0x7362);
-          const uint32_t y0 = __byte_perm(w[2][n], w[3][n], 0x5140), y1 = __byte_perm(w[2][n], w[3][n], 0x7362);
-          product(o[4 * n], bytes_f16(x0, 0x4140), bytes_f16(y0, 0x4140));
-          product(o[4 * n + 1], bytes_f16(x0, 0x4342), bytes_f16(y0, 0x4342));
-          product(o[4 * n + 2], bytes_f16(x1, 0x4140), bytes_f16(y1, 0x4140));
-          product(o[4 * n + 3], bytes_f16(x1, 0x4342), bytes_f16(y1, 0x4342));
-        } else {
-          // byte k of a word holds codes (0, 2), (4, 6), (1, 3), (5, 7) in its low and high half
-          constexpr int kSel[4] = {0x0400, 0x0501, 0x0602, 0x0703}, kLow[4] = {0, 4, 1, 5}, kUp[4] = {2, 6, 3, 7};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t x = __byte_perm(w[0][n], w[1][n], kSel[k]), y = __byte_perm(w[2][n], w[3][n], kSel[k]);
-            product(o[8 * n + kLow[k]], nibbles_f16<false>(x), nibbles_f16<false>(y));
-            product(o[8 * n + kUp[k]], nibbles_f16<true>(x), nibbles_f16<true>(y));
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t x = w[2 * e], y = w[2 * e + 1];
+          if constexpr (kBits == 8) {
+            product(o[2 * (q + e)], bytes_f16(x, 0x4240), bytes_f16(y, 0x4240));
+            product(o[2 * (q + e) + 1], bytes_f16(x, 0x4341), bytes_f16(y, 0x4341));
+          } else {
+            product(o[4 * (q + e)], nibbles_f16<false>(x), nibbles_f16<false>(y));
+            product(o[4 * (q + e) + 1], nibbles_f16<true>(x), nibbles_f16<true>(y));
+            product(o[4 * (q + e) + 2], nibbles_f16<false>(x >> 8), nibbles_f16<false>(y >> 8));
+            product(o[4 * (q + e) + 3], nibbles_f16<true>(x >> 8), nibbles_f16<true>(y >> 8));
           }
         }
       }
@@ -611,16 +603,18 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
       const float f = (top == minus_inf() ? 0.f : ex2(m[r] - top)) * (vref / kPScale);
       float* const row = sums + (warp * S::kHeads + g + 8 * r) * S::kPad;
 #pragma unroll
-      for (int n = 0; n < S::kCols; n += 4) {
-        // columns 2c and 2c + 1 of blocks n .. n + 3 are codes of lanes 2c's and 2c + 1's eighths of the vector
-        constexpr int kCodes = 32 / kBits;  // of a word
+      for (int n = 0; n < S::kCols; n += 8 / kBits * 2) {
+        // 8 bits: block 2q + e, column i is entry 16q + 2i + e, so this lane's two columns of two blocks are entries
+        // 16q + 4c .. + 3.  4 bits: block 4q + i, column 2j + e is entry 32q + 8j + 2i + e, so two blocks give four
+        // entries from 32q + 8c + 2i.
+        auto sum = [&](int k, int e) { return (kM == 1 ? o[k][e] + o[k][2 + e] : o[k][2 * r + e]) * f; };
+        if constexpr (kBits == 8) {
+          *reinterpret_cast<float4*>(row + 8 * n + 4 * c) = make_float4(sum(n, 0), sum(n + 1, 0), sum(n, 1), sum(n + 1, 1));
+        } else {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int d = word_byte<VP, 8>(n / kCodes, 2 * c + e) * 8 / kBits + n % kCodes;
-          float x[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = (kM == 1 ? o[n + k][e] + o[n + k][2 + e] : o[n + k][2 * r + e]) * f;
-          *reinterpret_cast<float4*>(row + d) = make_float4(x[0], x[1], x[2], x[3]);
+          for (int i = 0; i < 4; i += 2)
+            *reinterpret_cast<float4*>(row + 8 * n + 8 * c + 2 * i) =
+                make_float4(sum(n + i, 0), sum(n + i, 1), sum(n + i + 1, 0), sum(n + i + 1, 1));
         }
       }
     }
@@ -655,13 +649,16 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
 
 constexpr int kJoinWarps = 8;
 
-// Joins the parts of one row that several CTAs hold.  Few parts: a warp takes a head; many: all warps share a head's
-// parts.  A lane has four entries (and four more at 128).
-__global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const __grid_constant__ AttnArgs a, int heads_of_cta) {
+// Joins the parts of a row that several CTAs hold.  Few parts: a warp takes a head; many: all warps share a head's
+// parts.  A lane has four entries (and four more at 128).  A CTA takes a row, or a head where the rows are few.
+__global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const __grid_constant__ AttnArgs a, int heads_of_cta, int per_head) {
   __shared__ float s_num[kJoinWarps][256], s_den[kJoinWarps], s_top[kJoinWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.y;
   const int D = a.c.head_dim;
-  const uint32_t row = blockIdx.x, rows = gridDim.x, per_row = units_of(a, __ldg(a.lens + b));
+  // per_head: a CTA a head; else a CTA a row
+  const uint32_t rows = a.c.n_heads * a.head_chunks;
+  const uint32_t row = per_head ? blockIdx.x / a.group * a.head_chunks + blockIdx.x % a.group / heads_of_cta : blockIdx.x;
+  const uint32_t per_row = units_of(a, __ldg(a.lens + b));
   uint32_t before = 0, all = 0;  // units of the sequences before b, and of all
   for (int i = lane; i < a.batch; i += 32) {
     const uint32_t n = units_of(a, __ldg(a.lens + i));
@@ -677,37 +674,57 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const __grid_cons
   if (c0 == c1) return;  // one CTA had the whole row and has written it
   const int n = (int)(c1 - c0 + 1);
   const int kv = row / a.head_chunks, h0 = kv * a.group + row % a.head_chunks * heads_of_cta;
-  const int heads = min(heads_of_cta, (kv + 1) * a.group - h0);
+  const int h_from = per_head ? (int)blockIdx.x - h0 : 0, heads = per_head ? h_from + 1 : min(heads_of_cta, (kv + 1) * a.group - h0);
 
   float top, den;
   float4 num[2];
+  // parts s, s + every, ...: eight at a time, so that their loads are under way together
   auto add = [&](int h, int s, int every) {
     top = minus_inf(), den = 0.f;
     num[0] = num[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (; s < n; s += every) {
-      const int64_t at = ((int64_t)(c0 + s) * 2 + (s == 0 ? 1 : 0)) * heads_of_cta + h;
-      const float2 ml = a.ml[at];
-      float4 x[2];
+    for (; s < n; s += 8 * every) {
+      float2 ml[8];
+      float4 x[8];
+      auto at = [&](int j) {
+        const int t = min(s + j * every, n - 1);  // behind the last part: read, and not used
+        return ((int64_t)(c0 + t) * 2 + (t == 0 ? 1 : 0)) * heads_of_cta + h;
+      };
+      auto load = [&](int k) {
+        if (4 * lane + 128 * k < D)
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        x[k] = 4 * lane + 128 * k < D ? *reinterpret_cast<const float4*>(a.part + at * D + 4 * lane + 128 * k)
-                                      : make_float4(0.f, 0.f, 0.f, 0.f);
-      const float up = fmaxf(top, ml.x), ref = up == minus_inf() ? 0.f : up;
-      const float f = ex2(top - ref), g = ex2(ml.x - ref);
+          for (int j = 0; j < 8; ++j) x[j] = *reinterpret_cast<const float4*>(a.part + at(j) * D + 4 * lane + 128 * k);
+      };
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ml[j] = a.ml[at(j)];
+      load(0);
+      float up = top;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) up = fmaxf(up, ml[j].x);
+      const float ref = up == minus_inf() ? 0.f : up, f = ex2(top - ref);
+      float w[8];
       top = up;
-      den = den * f + g * ml.y;
+      den *= f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool on = s + j * every < n;
+        w[j] = on ? ex2(ml[j].x - ref) : 0.f;
+        den += on ? w[j] * ml[j].y : 0.f;
+      }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        num[k].x = num[k].x * f + g * x[k].x, num[k].y = num[k].y * f + g * x[k].y;
-        num[k].z = num[k].z * f + g * x[k].z, num[k].w = num[k].w * f + g * x[k].w;
+        if (4 * lane + 128 * k >= D) break;
+        if (k) load(k);
+        num[k].x *= f, num[k].y *= f, num[k].z *= f, num[k].w *= f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          num[k].x += w[j] * x[j].x, num[k].y += w[j] * x[j].y, num[k].z += w[j] * x[j].z, num[k].w += w[j] * x[j].w;
       }
     }
   };
   auto write_lse = [&](int h, float ref, float sum) {
     if (a.lse) a.lse[b * a.lse_batch + h0 + h] = kLn2 * ((ref == minus_inf() ? 0.f : ref) + log2f(sum));
   };
-  if (n <= 2 * kJoinWarps) {
+  if (n <= kJoinWarps && !per_head) {
     for (int h = warp; h < heads; h += kJoinWarps) {
       add(h, 0, 1);
       const float f = 1.f / den;
@@ -720,7 +737,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const __grid_cons
     }
     return;
   }
-  for (int h = 0; h < heads; ++h) {
+  for (int h = h_from; h < heads; ++h) {
     add(h, warp, kJoinWarps);
     if (lane == 0) s_den[warp] = den, s_top[warp] = top;
 #pragma unroll
@@ -749,45 +766,63 @@ int heads_of_cta(int group) { return group > 8 ? 16 : 8; }
 int64_t most_units(int64_t batch, int64_t rows, int64_t limit) { return batch * rows * ((limit + kUnit - 1) / kUnit); }
 bool has_parts(int64_t limit) { return limit > kUnit; }
 
+// What launch_main does: fill in a.ctas only; launch with room for `bytes` of workspace (IMQ_ERR_BUFFER if that is
+// too little).
+struct Launch {
+  bool only_count;
+  void* workspace;
+  size_t bytes;
+  cudaStream_t st;
+};
+
+size_t workspace_of(const AttnArgs& a) {
+  return has_parts(a.limit) ? (size_t)a.ctas * 2 * heads_of_cta(a.group) * ((size_t)a.c.head_dim * 4 + 8) : 0;
+}
+
 template <int kBits, int kD, int kM>
-imq_status launch_shape(AttnArgs& a, int num_sms, int64_t rows, bool only_count, cudaStream_t st) {
+imq_status launch_shape(AttnArgs& a, int num_sms, int64_t rows, const Launch& l) {
   constexpr int kSmem = Shape<kBits, kD, kM>::kSmem;
   const void* fn = reinterpret_cast<const void*>(&k_attn<kBits, kD, kM>);
-  if (ensure_smem(fn, kSmem) != cudaSuccess) return IMQ_ERR_CUDA;
-  int per_sm = 0;
-  if (blocks_per_sm(fn, kWarps * 32, kSmem, &per_sm) != cudaSuccess || per_sm < 1) return IMQ_ERR_CUDA;
+  static std::atomic<int> resident[64];  // CTAs an SM holds, per device; 0: not asked yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return IMQ_ERR_CUDA;
+  int per_sm = resident[dev].load(std::memory_order_acquire);
+  if (per_sm == 0) {
+    if (ensure_smem(fn, kSmem) != cudaSuccess || blocks_per_sm(fn, kWarps * 32, kSmem, &per_sm) != cudaSuccess || per_sm < 1)
+      return IMQ_ERR_CUDA;
+    resident[dev].store(per_sm, std::memory_order_release);
+  }
   const int64_t most = most_units(a.batch, rows, a.limit);
   a.ctas = (int)(most < 1 ? 1 : most < (int64_t)per_sm * num_sms ? most : (int64_t)per_sm * num_sms);
-  if (only_count) return IMQ_OK;
-  k_attn<kBits, kD, kM><<<a.ctas, kWarps * 32, kSmem, st>>>(a);
+  if (l.only_count) return IMQ_OK;
+  if (has_parts(a.limit)) {
+    if (!l.workspace || l.bytes < workspace_of(a)) return IMQ_ERR_BUFFER;
+    a.part = static_cast<float*>(l.workspace);
+    a.ml = reinterpret_cast<float2*>(a.part + (size_t)a.ctas * 2 * (8 * kM) * kD);
+  }
+  k_attn<kBits, kD, kM><<<a.ctas, kWarps * 32, kSmem, l.st>>>(a);
   return cudaGetLastError() == cudaSuccess ? IMQ_OK : IMQ_ERR_CUDA;
 }
 
 template <int kBits, int kM>
-imq_status launch_dim(AttnArgs& a, int num_sms, int64_t rows, bool only_count, cudaStream_t st) {
+imq_status launch_dim(AttnArgs& a, int num_sms, int64_t rows, const Launch& l) {
   switch (a.c.head_dim) {
-    case 64: return launch_shape<kBits, 64, kM>(a, num_sms, rows, only_count, st);
-    case 128: return launch_shape<kBits, 128, kM>(a, num_sms, rows, only_count, st);
-    case 192: return launch_shape<kBits, 192, kM>(a, num_sms, rows, only_count, st);
-    default: return launch_shape<kBits, 256, kM>(a, num_sms, rows, only_count, st);
+    case 64: return launch_shape<kBits, 64, kM>(a, num_sms, rows, l);
+    case 128: return launch_shape<kBits, 128, kM>(a, num_sms, rows, l);
+    case 192: return launch_shape<kBits, 192, kM>(a, num_sms, rows, l);
+    default: return launch_shape<kBits, 256, kM>(a, num_sms, rows, l);
   }
 }
 
-// Fills in a.ctas and, unless only that is asked for, launches k_attn.
-imq_status launch_main(AttnArgs& a, bool only_count, cudaStream_t st) {
+imq_status launch_main(AttnArgs& a, const Launch& l) {
   DeviceState* ds;
   const imq_status s = device_state(&ds);
   if (s != IMQ_OK) return s;
   a.status = ds->status;
   const int64_t rows = (int64_t)a.head_chunks * a.c.n_heads;
   const bool wide = heads_of_cta(a.group) == 16;
-  if (a.c.bits == 4)
-    return wide ? launch_dim<4, 2>(a, ds->num_sms, rows, only_count, st) : launch_dim<4, 1>(a, ds->num_sms, rows, only_count, st);
-  return wide ? launch_dim<8, 2>(a, ds->num_sms, rows, only_count, st) : launch_dim<8, 1>(a, ds->num_sms, rows, only_count, st);
-}
-
-size_t workspace_of(const AttnArgs& a) {
-  return has_parts(a.limit) ? (size_t)a.ctas * 2 * heads_of_cta(a.group) * ((size_t)a.c.head_dim * 4 + 8) : 0;
+  if (a.c.bits == 4) return wide ? launch_dim<4, 2>(a, ds->num_sms, rows, l) : launch_dim<4, 1>(a, ds->num_sms, rows, l);
+  return wide ? launch_dim<8, 2>(a, ds->num_sms, rows, l) : launch_dim<8, 1>(a, ds->num_sms, rows, l);
 }
 
 imq_status check_shape(const imq_kv_cache* c, int64_t batch, int32_t q_heads, int64_t max_len) {
@@ -809,7 +844,7 @@ imq_status paged_attention_workspace(const imq_kv_cache* c, int64_t batch, int32
   a.c = *c, a.batch = (int)batch, a.limit = (int)max_len, a.group = q_heads / c->n_heads;
   const int per = heads_of_cta(a.group);
   a.head_chunks = (a.group + per - 1) / per;
-  s = launch_main(a, true, nullptr);
+  s = launch_main(a, {true, nullptr, 0, nullptr});
   if (s == IMQ_OK) *bytes = workspace_of(a);
   return s;
 }
@@ -844,26 +879,20 @@ imq_status launch_paged_attention(const imq_kv_cache* c, const void* Q, imq_dtyp
   a.scale = scale;
   a.out = out, a.o_batch = o_batch, a.o_head = o_head, a.o_bf16 = ot == IMQ_BF16;
   a.lse = lse, a.lse_batch = lse_batch;
-  if (has_parts(max_len)) {
-    s = launch_main(a, true, st);
-    if (s != IMQ_OK) return s;
-    if (!workspace || workspace_bytes < workspace_of(a)) return IMQ_ERR_BUFFER;
-    a.part = static_cast<float*>(workspace);
-    a.ml = reinterpret_cast<float2*>(a.part + (size_t)a.ctas * 2 * per * c->head_dim);
-  }
-  s = launch_main(a, false, st);
+  s = launch_main(a, {false, workspace, workspace_bytes, st});
   if (s != IMQ_OK || !has_parts(max_len)) return s;
   // launched before k_attn has finished; it waits for it on the device
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.head_chunks * c->n_heads), (unsigned)batch);
+  const int rows = a.head_chunks * c->n_heads, per_head = batch * q_heads <= 2 * a.ctas;
+  cfg.gridDim = dim3((unsigned)(per_head ? q_heads : rows), (unsigned)batch);
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_attn_join, a, per) == cudaSuccess ? IMQ_OK : IMQ_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, k_attn_join, a, per, per_head) == cudaSuccess ? IMQ_OK : IMQ_ERR_CUDA;
 }
 
 }  // namespace imq

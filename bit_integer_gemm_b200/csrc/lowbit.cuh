@@ -114,14 +114,14 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Signed by unsigned bytes, 32-bit integer sums: D = C + A (16 x 32) * B (32 x 8); a0 / b0 hold inner positions
+// Signed by unsigned bytes, 32-bit integer sums: D += A (16 x 32) * B (32 x 8); a0 / b0 hold inner positions
 // 4c .. 4c + 3 and a2 / b1 16 + 4c .. + 3, a byte each; a1, a3 row g + 8.
 __device__ __forceinline__ void mma_s8u8(int32_t (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1, int32_t c0, int32_t c1, int32_t c2, int32_t c3) {
+                                         uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.s32.s8.u8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
-      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(c0), "r"(c1), "r"(c2), "r"(c3));
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.u8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // Codes as fp16 or bf16 pairs without integer-to-float conversions: a code's bits are set into the mantissa
@@ -154,17 +154,32 @@ __device__ __forceinline__ uint32_t nibbles_bf16(uint32_t w) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// Two 8 x 8 blocks of 16-bit elements and the next two, transposed on the way: lane i gives the address of row
+// i % 8 of block i / 8 (16 bytes), and gets of each block the elements of rows 2c and 2c + 1 in column g.
+__device__ __forceinline__ void ldmatrix_trans4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
 // ------------------------------------------------------------------------------------------------
-// asynchronous copies, each thread's own bytes; src_bytes 0 writes zeros and reads nothing
+// asynchronous copies, each thread's own bytes
 // ------------------------------------------------------------------------------------------------
 template <int kBytes>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, uint32_t src_bytes) {
-  if (kBytes == 16) {
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes) : "memory");
+}
+// src_bytes 0 writes zeros and reads nothing.
+template <int kBytes>
+__device__ __forceinline__ void cp_async_part(uint32_t dst, const void* src, uint32_t src_bytes) {
+  if constexpr (kBytes == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
-  } else {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(src_bytes)
-                 : "memory");
-  }
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(src_bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kPending>

@@ -5,6 +5,8 @@
 // e = r % 8 of word 4 * ((r % 32) / 8) + r / 32 of the block's 16.  A lane that takes the 16 bytes at
 // 16 * c of a block holds the inputs 32h + 8c .. 32h + 8c + 7 for h = 0..3: one word per 32 inputs, so a
 // group of 32 ends at a word, and the inputs it needs from a token are 16 contiguous bytes of bf16 per word.
+#include <atomic>
+
 #include "lowbit.cuh"
 #include "internal.h"
 
@@ -162,12 +164,23 @@ __global__ void __launch_bounds__(256) k_w4_dequantize_cols(DequantArgs a) {
 // ------------------------------------------------------------------------------------------------
 // Y = X * W for a few tokens
 // ------------------------------------------------------------------------------------------------
+// Bound: the weight is read once, N K / 2 bytes and the steps, for 2 M N K operations -- memory, as long as turning
+// codes into operands keeps up: eleven instructions for eight codes.  So the product runs on the warp-level tensor
+// core instruction with the weight as the 16-row operand: a conversion serves 8 tokens at once.
+//   - Codes in -7 .. 7 are exact in bf16, and bf16 entries of X are operands as they are.
+//   - An fp32 entry is cut into three bf16 parts of 8 bits, exact together: a column of the other operand for each
+//     part with up to 2 tokens, an operand for each part with more.
+//   - The sums of a group are scaled by its step in fp32.
+// A CTA takes 16 kR output channels at a time; its eight warps take the blocks of 128 inputs in turn, each with its own
+// ring of asynchronous copies (every lane copies the 16-byte pieces that it will use itself) that runs on from one
+// set of channels to the next.  The warps' sums meet in shared memory, in a fixed order.
 struct MatvecArgs {
   const uint8_t* codes;
   int64_t ldc;
   const float* steps;
   int64_t lds;
   int64_t K, N;
+  int group;
   const void* X;
   int64_t ldx;
   int64_t M;
@@ -180,131 +193,223 @@ struct MatvecArgs {
 constexpr int kTokens = 16;  // tokens of a CTA
 constexpr int kMvWarps = 8;
 
-// The B operand of 8 inputs of one token (or part of one): four bf16 pairs.  bf16 entries go as they are;
-// an fp32 entry is cut into three bf16 parts of 8 bits, exact together, `part` of which this column holds.
-__device__ __forceinline__ uint4 x_pairs(const __nv_bfloat16* p, int64_t k0, int64_t K, bool vec, int) {
-  if (vec && k0 + 8 <= K) return *reinterpret_cast<const uint4*>(p + k0);
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t k = k0 + 2 * i;
-    const uint32_t lo = k < K ? __bfloat16_as_ushort(p[k]) : 0u, hi = k + 1 < K ? __bfloat16_as_ushort(p[k + 1]) : 0u;
-    w[i] = lo | (hi << 16);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ uint4 x_pairs(const float* p, int64_t k0, int64_t K, bool vec, int part) {
-  float x[8];
-  if (vec && k0 + 8 <= K) {
-    load8(p + k0, x);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = k0 + e < K ? p[k0 + e] : 0.f;
-  }
-  const uint32_t m1 = part >= 1 ? 0xFFFF0000u : 0u, m2 = part >= 2 ? 0xFFFF0000u : 0u;
-  uint32_t w[4];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    x[e] -= __uint_as_float(__float_as_uint(x[e]) & m1);
-    x[e] -= __uint_as_float(__float_as_uint(x[e]) & m2);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = __byte_perm(__float_as_uint(x[2 * i]), __float_as_uint(x[2 * i + 1]), 0x7632);
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
+// kTiles: operands of 8 columns.  bf16: tokens 8t + g.  fp32: 1: part g % 3 of token g / 3; 3 (6): parts 0-2 of token g
+// (and of token g + 8).
+template <typename T, int kTiles, int kR>
+struct MvShape {
+  static constexpr bool kF32 = sizeof(T) == 4;
+  static constexpr bool kPacked = kF32 && kTiles == 1;
+  static constexpr int kParts = kF32 ? 3 : 1;
+  static constexpr int kTok = kPacked ? 1 : kTiles / kParts;  // tokens of a lane
+  static constexpr int kXPieces = kTok * 4 * (kF32 ? 2 : 1);  // 16-byte pieces of X of a lane and block
+  static constexpr int kStage = (2 * kR + kXPieces) * 512 + 2 * kR * 128;
+  static constexpr int kStages = 12000 / kStage < 2 ? 2 : 12000 / kStage > 6 ? 6 : 12000 / kStage;
+  static constexpr int kCols = kTiles * 8 + 1;
+  static constexpr int kRed = kMvWarps * 16 * kR * kCols * 4;
+  static constexpr int kSmem = kMvWarps * kStages * kStage + kRed;
+};
 
-// One CTA: 16 output channels, up to 16 tokens.  Its warps take the blocks of 128 inputs in turn; the codes
-// become bf16 in registers (exact) and are the A operand, the tokens' entries the B operand, so up to 8
-// columns cost no more than one.  A group's sum is scaled by its step in fp32.  The warps' sums meet in
-// shared memory in a fixed order.
-template <typename T, int kGroup, int kTiles>
-__global__ void __launch_bounds__(kMvWarps * 32) k_w4_matvec(MatvecArgs a) {
-  constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
-  __shared__ float red[kMvWarps][16][kTiles * 8 + 1];
+template <typename T, int kTiles, int kR>
+__global__ void __launch_bounds__(kMvWarps * 32, kTiles * kR <= 2 ? 2 : 1) k_w4_matvec(const __grid_constant__ MatvecArgs a) {
+  using S = MvShape<T, kTiles, kR>;
+  constexpr int kStages = S::kStages, kPer16 = 16 / sizeof(T);
+  extern __shared__ __align__(16) uint8_t smem[];
+  float* const red = reinterpret_cast<float*>(smem + kMvWarps * kStages * S::kStage);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-  const int64_t n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * kTokens;
+  const int K = (int)a.K, N = (int)a.N, nb = (K + kBlock - 1) / kBlock;
+  const int64_t m0 = (int64_t)blockIdx.y * kTokens;
   const int tokens = (int)min((int64_t)kTokens, a.M - m0);
-  // rows behind the last one read the last one; their sums are not stored
-  const int64_t r0 = min(n0 + g, a.N - 1), r1 = min(n0 + g + 8, a.N - 1);
-  const uint8_t* w0 = a.codes + r0 * a.ldc + 16 * c;
-  const uint8_t* w1 = a.codes + r1 * a.ldc + 16 * c;
-  const float* s0 = a.steps + r0 * a.lds;
-  const float* s1 = a.steps + r1 * a.lds;
-  const T* xp[kTiles];
-  int part[kTiles];
-  bool has[kTiles];
+  const int sets = (N + 16 * kR - 1) / (16 * kR);
+  const int per_set = (nb - warp + kMvWarps - 1) / kMvWarps;  // this warp's blocks of a set (0 for K below its first)
+  const int groups = (K + a.group - 1) / a.group, per_block = kBlock / a.group;
+  uint8_t* const mine = smem + warp * kStages * S::kStage;
+
+  const T* xp[S::kTok];
+  bool has[S::kTok];
 #pragma unroll
-  for (int t = 0; t < kTiles; ++t) {
-    const int col = 8 * t + g, tok = col / kParts;
-    part[t] = col % kParts;
+  for (int t = 0; t < S::kTok; ++t) {
+    const int tok = S::kPacked ? g / 3 : 8 * t + g;
     has[t] = tok < tokens;
     xp[t] = static_cast<const T*>(a.X) + (m0 + (has[t] ? tok : 0)) * a.ldx;
   }
-  float total[kTiles][4] = {}, acc[kTiles][4] = {};
-  const int64_t nb = (a.K + kBlock - 1) / kBlock;
-  for (int64_t kb = warp; kb < nb; kb += kMvWarps) {
-    const uint4 v0 = __ldg(reinterpret_cast<const uint4*>(w0 + kb * kBlockBytes));
-    const uint4 v1 = __ldg(reinterpret_cast<const uint4*>(w1 + kb * kBlockBytes));
-    const uint32_t p0[4] = {v0.x, v0.y, v0.z, v0.w}, p1[4] = {v1.x, v1.y, v1.z, v1.w};
+  // columns without a token stay zero
+  for (int i = lane; i < kStages * S::kStage / 16; i += 32) reinterpret_cast<uint4*>(mine)[i] = make_uint4(0u, 0u, 0u, 0u);
+
+  // the next block to copy: set, its block, ring stage
+  int set_in = blockIdx.x, block_in = 0, stage_in = 0;
+  auto issue = [&]() {
+    if (set_in < sets && per_set > 0) {
+      const int kb = warp + block_in * kMvWarps;
+      uint8_t* const to = mine + stage_in * S::kStage;
+      const uint32_t dst = smem_addr(to) + lane * 16;
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      const int64_t k0 = kb * kBlock + 32 * h + 8 * c;
-      uint32_t q0[4], q1[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        q0[i] = nibbles_bf16(p0[h] >> (4 * i));
-        q1[i] = nibbles_bf16(p1[h] >> (4 * i));
+      for (int r = 0; r < 2 * kR; ++r) {
+        // rows behind the last one read the last one; their sums are not stored
+        const int64_t n = min((int64_t)set_in * 16 * kR + 8 * r + g, (int64_t)N - 1);
+        cp_async<16>(dst + r * 512, a.codes + n * a.ldc + kb * kBlockBytes + 16 * c);
+        const int gi = kb * per_block + c;
+        if (c < per_block && gi < groups)
+          cp_async<4>(smem_addr(to) + (2 * kR + S::kXPieces) * 512 + r * 128 + lane * 4, a.steps + n * a.lds + gi);
       }
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
-        const uint4 x = has[t] ? x_pairs(xp[t], k0, a.K, a.aligned, part[t]) : make_uint4(0u, 0u, 0u, 0u);
-        mma_bf16(acc[t], q0[0], q1[0], q0[1], q1[1], x.x, x.y);
-        mma_bf16(acc[t], q0[2], q1[2], q0[3], q1[3], x.z, x.w);
-      }
-      if ((h + 1) * 32 % kGroup == 0) {
-        const int64_t gi = (kb * kBlock + 32 * h) / kGroup;
-        if (gi * kGroup < a.K) {
-          const float d0 = __ldg(s0 + gi), d1 = __ldg(s1 + gi);
+      for (int t = 0; t < S::kTok; ++t)
+        if (has[t]) {
 #pragma unroll
-          for (int t = 0; t < kTiles; ++t) {
-            total[t][0] += d0 * acc[t][0], total[t][1] += d0 * acc[t][1];
-            total[t][2] += d1 * acc[t][2], total[t][3] += d1 * acc[t][3];
+          for (int h = 0; h < 4; ++h) {
+            const int k0 = kb * kBlock + 32 * h + 8 * c;
+            constexpr int kPieces = 8 / kPer16;  // of eight entries
+            const int at = 2 * kR + (t * 4 + h) * kPieces;
+            if (a.aligned && k0 + 8 <= K) {
+#pragma unroll
+              for (int q = 0; q < kPieces; ++q) cp_async<16>(dst + (at + q) * 512, xp[t] + k0 + q * kPer16);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                reinterpret_cast<T*>(to + (at + e / kPer16) * 512 + lane * 16)[e % kPer16] = k0 + e < K ? xp[t][k0 + e] : from_f32<T>(0.f);
+            }
           }
         }
+      stage_in = stage_in + 1 == kStages ? 0 : stage_in + 1;
+      if (++block_in == per_set) block_in = 0, set_in += gridDim.x;
+    }
+    cp_async_commit();
+  };
+  for (int i = 0; i < kStages - 1; ++i) issue();
+
+  int stage = 0;
+  for (int set = blockIdx.x; set < sets; set += gridDim.x) {
+    float total[kR][kTiles][4] = {};
+    for (int i = 0; i < per_set; ++i) {
+      cp_async_wait<kStages - 2>();
+      __syncwarp();  // the steps were copied by other lanes; every lane is done with the stage that is overwritten now
+      issue();
+      const uint8_t* const from = mine + stage * S::kStage;
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      uint4 v[kR][2];
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+      for (int r = 0; r < kR; ++r)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) v[r][j] = *reinterpret_cast<const uint4*>(from + (2 * r + j) * 512 + lane * 16);
+      const float* const st = reinterpret_cast<const float*>(from + (2 * kR + S::kXPieces) * 512);
+      float acc[kR][kTiles][4];
+      int gi = 0;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        // the other operand: per tile, the pairs of this half's first four inputs and of its second four
+        uint32_t x[kTiles][4];
+#pragma unroll
+        for (int t = 0; t < S::kTok; ++t) {
+          if constexpr (!S::kF32) {
+            const uint4 q = *reinterpret_cast<const uint4*>(from + (2 * kR + t * 4 + h) * 512 + lane * 16);
+            x[t][0] = q.x, x[t][1] = q.y, x[t][2] = q.z, x[t][3] = q.w;
+          } else {
+            float f[8];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const float4 y = *reinterpret_cast<const float4*>(from + (2 * kR + (t * 4 + h) * 2 + q) * 512 + lane * 16);
+              f[4 * q] = y.x, f[4 * q + 1] = y.y, f[4 * q + 2] = y.z, f[4 * q + 3] = y.w;
+            }
+            if constexpr (S::kPacked) {
+              const uint32_t m1 = g % 3 >= 1 ? 0xFFFF0000u : 0u, m2 = g % 3 >= 2 ? 0xFFFF0000u : 0u;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                f[e] -= __uint_as_float(__float_as_uint(f[e]) & m1);
+                f[e] -= __uint_as_float(__float_as_uint(f[e]) & m2);
+              }
+            }
+#pragma unroll
+            for (int part = 0; part < (S::kPacked ? 1 : 3); ++part) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                x[t * (S::kPacked ? 1 : 3) + part][e] = __byte_perm(__float_as_uint(f[2 * e]), __float_as_uint(f[2 * e + 1]), 0x7632);
+              if (part < 2) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] -= __uint_as_float(__float_as_uint(f[e]) & 0xFFFF0000u);
+              }
+            }
+          }
+        }
+        const bool opens = h * 32 % a.group == 0, closes = (h + 1) * 32 % a.group == 0;
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+          const uint32_t p0 = h == 0 ? v[r][0].x : h == 1 ? v[r][0].y : h == 2 ? v[r][0].z : v[r][0].w;
+          const uint32_t p1 = h == 0 ? v[r][1].x : h == 1 ? v[r][1].y : h == 2 ? v[r][1].z : v[r][1].w;
+          uint32_t q0[4], q1[4];
+#pragma unroll
+          for (int i4 = 0; i4 < 4; ++i4) q0[i4] = nibbles_bf16(p0 >> (4 * i4)), q1[i4] = nibbles_bf16(p1 >> (4 * i4));
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t) {
+            if (opens) acc[r][t][0] = acc[r][t][1] = acc[r][t][2] = acc[r][t][3] = 0.f;
+            mma_bf16(acc[r][t], q0[0], q1[0], q0[1], q1[1], x[t][0], x[t][1]);
+            mma_bf16(acc[r][t], q0[2], q1[2], q0[3], q1[3], x[t][2], x[t][3]);
+          }
+          if (closes) {
+            const float d0 = st[(2 * r) * 32 + g * 4 + gi], d1 = st[(2 * r + 1) * 32 + g * 4 + gi];
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+              total[r][t][0] += d0 * acc[r][t][0], total[r][t][1] += d0 * acc[r][t][1];
+              total[r][t][2] += d1 * acc[r][t][2], total[r][t][3] += d1 * acc[r][t][3];
+            }
+          }
+        }
+        if (closes) ++gi;
       }
     }
-  }
+    // ---- the warps' sums of this set
 #pragma unroll
-  for (int t = 0; t < kTiles; ++t) {
-    red[warp][g][8 * t + 2 * c] = total[t][0], red[warp][g][8 * t + 2 * c + 1] = total[t][1];
-    red[warp][g + 8][8 * t + 2 * c] = total[t][2], red[warp][g + 8][8 * t + 2 * c + 1] = total[t][3];
-  }
-  __syncthreads();
-  for (int o = threadIdx.x; o < 16 * tokens; o += kMvWarps * 32) {
-    const int r = o & 15, tok = o >> 4;
-    if (n0 + r >= a.N) continue;
-    float y = 0.f;
+    for (int r = 0; r < kR; ++r)
 #pragma unroll
-    for (int p = kParts - 1; p >= 0; --p)  // the smallest parts first
-      for (int w = 0; w < kMvWarps; ++w) y += red[w][r][tok * kParts + p];
-    const int64_t at = (m0 + tok) * a.ldy + n0 + r;
-    if (a.y_bf16)
-      static_cast<__nv_bfloat16*>(a.Y)[at] = __float2bfloat16_rn(y);
-    else
-      static_cast<float*>(a.Y)[at] = y;
+      for (int t = 0; t < kTiles; ++t) {
+        float* const at = red + (warp * 16 * kR + 16 * r + g) * S::kCols + 8 * t + 2 * c;
+        at[0] = total[r][t][0], at[1] = total[r][t][1];
+        at[8 * S::kCols] = total[r][t][2], at[8 * S::kCols + 1] = total[r][t][3];
+      }
+    __syncthreads();
+    for (int o = threadIdx.x; o < 16 * kR * tokens; o += kMvWarps * 32) {
+      const int row = o % (16 * kR), tok = o / (16 * kR), n = set * 16 * kR + row;
+      float y = 0.f;
+#pragma unroll
+      for (int p = S::kParts - 1; p >= 0; --p) {  // the smallest parts first
+        const int col = S::kPacked ? 3 * tok + p : S::kF32 ? (tok / 8 * 3 + p) * 8 + tok % 8 : tok;
+#pragma unroll
+        for (int w = 0; w < kMvWarps; ++w) y += red[(w * 16 * kR + row) * S::kCols + col];
+      }
+      if (n < N) {
+        const int64_t at = (m0 + tok) * a.ldy + n;
+        if (a.y_bf16)
+          static_cast<__nv_bfloat16*>(a.Y)[at] = __float2bfloat16_rn(y);
+        else
+          static_cast<float*>(a.Y)[at] = y;
+      }
+    }
+    __syncthreads();
   }
+  cp_async_wait<0>();
 }
 
+template <typename T, int kTiles, int kR>
+imq_status matvec_shape(const MatvecArgs& a, int num_sms, cudaStream_t st) {
+  constexpr int kSmem = MvShape<T, kTiles, kR>::kSmem;
+  const void* fn = reinterpret_cast<const void*>(&k_w4_matvec<T, kTiles, kR>);
+  static std::atomic<int> resident[64];  // CTAs an SM holds, per device; 0: not asked yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return IMQ_ERR_CUDA;
+  int per_sm = resident[dev].load(std::memory_order_acquire);
+  if (per_sm == 0) {
+    if (ensure_smem(fn, kSmem) != cudaSuccess || blocks_per_sm(fn, kMvWarps * 32, kSmem, &per_sm) != cudaSuccess || per_sm < 1)
+      return IMQ_ERR_CUDA;
+    resident[dev].store(per_sm, std::memory_order_release);
+  }
+  const int64_t sets = (a.N + 16 * kR - 1) / (16 * kR), most = (int64_t)per_sm * num_sms;
+  const dim3 grid((unsigned)(sets < most ? sets : most), (unsigned)((a.M + kTokens - 1) / kTokens));
+  k_w4_matvec<T, kTiles, kR><<<grid, kMvWarps * 32, kSmem, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? IMQ_OK : IMQ_ERR_CUDA;
+}
+
+// Two sets of 16 channels at a time where there are enough of them for every SM: X is read and cut up half as often.
 template <typename T, int kTiles>
-void matvec_group(const MatvecArgs& a, int group, dim3 grid, cudaStream_t st) {
-  if (group == 32)
-    k_w4_matvec<T, 32, kTiles><<<grid, kMvWarps * 32, 0, st>>>(a);
-  else if (group == 64)
-    k_w4_matvec<T, 64, kTiles><<<grid, kMvWarps * 32, 0, st>>>(a);
-  else
-    k_w4_matvec<T, 128, kTiles><<<grid, kMvWarps * 32, 0, st>>>(a);
+imq_status matvec_rows(const MatvecArgs& a, int num_sms, cudaStream_t st) {
+  return a.N > 32 * num_sms ? matvec_shape<T, kTiles, 2>(a, num_sms, st) : matvec_shape<T, kTiles, 1>(a, num_sms, st);
 }
 
 bool is_float(imq_dtype t) { return t == IMQ_F32 || t == IMQ_BF16; }
@@ -392,23 +497,17 @@ imq_status launch_w4_matvec(const uint8_t* codes, int64_t ldc, const float* step
   if ((K > 0 && !X) || !Y || (reinterpret_cast<uintptr_t>(X) & (size_of(xt) - 1)) ||
       (reinterpret_cast<uintptr_t>(Y) & (size_of(yt) - 1)))
     return IMQ_ERR_ARG;
-  MatvecArgs a{codes, ldc, steps, lds, K, N, X, ldx, M, Y, ldy, yt == IMQ_BF16,
+  DeviceState* ds;
+  s = device_state(&ds);
+  if (s != IMQ_OK) return s;
+  MatvecArgs a{codes, ldc, steps, lds, K, N, group, X, ldx, M, Y, ldy, yt == IMQ_BF16,
                aligned16(X) && (M == 1 || ldx * size_of(xt) % 16 == 0)};
-  const dim3 grid((unsigned)((N + 15) / 16), (unsigned)((M + kTokens - 1) / kTokens));
-  const int cols = (int)(M < kTokens ? M : kTokens) * (xt == IMQ_F32 ? 3 : 1), tiles = (cols + 7) / 8;
-  if (xt == IMQ_BF16) {
-    if (tiles == 1)
-      matvec_group<__nv_bfloat16, 1>(a, group, grid, st);
-    else
-      matvec_group<__nv_bfloat16, 2>(a, group, grid, st);
-  } else if (tiles == 1) {
-    matvec_group<float, 1>(a, group, grid, st);
-  } else if (tiles <= 3) {
-    matvec_group<float, 3>(a, group, grid, st);
-  } else {
-    matvec_group<float, 6>(a, group, grid, st);
-  }
-  return launched();
+  const int64_t tokens = M < kTokens ? M : kTokens;
+  if (xt == IMQ_BF16)
+    return tokens <= 8 ? matvec_rows<__nv_bfloat16, 1>(a, ds->num_sms, st) : matvec_rows<__nv_bfloat16, 2>(a, ds->num_sms, st);
+  return tokens <= 2   ? matvec_rows<float, 1>(a, ds->num_sms, st)
+         : tokens <= 8 ? matvec_rows<float, 3>(a, ds->num_sms, st)
+                       : matvec_rows<float, 6>(a, ds->num_sms, st);
 }
 
 }  // namespace imq
