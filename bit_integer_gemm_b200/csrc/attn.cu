@@ -72,6 +72,7 @@ struct AttnArgs {
   float* part;        // [CTA][2][head of the row][D]: sums of rows that several CTAs share
   float2* ml;         // [CTA][2][head of the row]: reference (a power of two's exponent) and sum of the weights
   int32_t* status;
+  uint32_t one;       // kOneF16
 };
 
 // Bytes a lane holds of a token's key (a quarter of the vector), as 16-byte pieces and an 8-byte one.  Piece p of the
@@ -570,13 +571,13 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
         for (int e = 0; e < 2; ++e) {
           const uint32_t x = w[2 * e], y = w[2 * e + 1];
           if constexpr (kBits == 8) {
-            product(o[2 * (q + e)], bytes_f16(x, 0x4240), bytes_f16(y, 0x4240));
-            product(o[2 * (q + e) + 1], bytes_f16(x, 0x4341), bytes_f16(y, 0x4341));
+            product(o[2 * (q + e)], bytes_f16(x, 0x5250, a.one), bytes_f16(y, 0x5250, a.one));
+            product(o[2 * (q + e) + 1], bytes_f16(x, 0x5351, a.one), bytes_f16(y, 0x5351, a.one));
           } else {
-            product(o[4 * (q + e)], nibbles_f16<false>(x), nibbles_f16<false>(y));
-            product(o[4 * (q + e) + 1], nibbles_f16<true>(x), nibbles_f16<true>(y));
-            product(o[4 * (q + e) + 2], nibbles_f16<false>(x >> 8), nibbles_f16<false>(y >> 8));
-            product(o[4 * (q + e) + 3], nibbles_f16<true>(x >> 8), nibbles_f16<true>(y >> 8));
+            product(o[4 * (q + e)], nibbles_f16<false>(x, a.one), nibbles_f16<false>(y, a.one));
+            product(o[4 * (q + e) + 1], nibbles_f16<true>(x, a.one), nibbles_f16<true>(y, a.one));
+            product(o[4 * (q + e) + 2], nibbles_f16<false>(x >> 8, a.one), nibbles_f16<false>(y >> 8, a.one));
+            product(o[4 * (q + e) + 3], nibbles_f16<true>(x >> 8, a.one), nibbles_f16<true>(y >> 8, a.one));
           }
         }
       }
@@ -818,7 +819,7 @@ imq_status launch_main(AttnArgs& a, const Launch& l) {
   DeviceState* ds;
   const imq_status s = device_state(&ds);
   if (s != IMQ_OK) return s;
-  a.status = ds->status;
+  a.status = ds->status, a.one = kOneF16;
   const int64_t rows = (int64_t)a.head_chunks * a.c.n_heads;
   const bool wide = heads_of_cta(a.group) == 16;
   if (a.c.bits == 4) return wide ? launch_dim<4, 2>(a, ds->num_sms, rows, l) : launch_dim<4, 1>(a, ds->num_sms, rows, l);

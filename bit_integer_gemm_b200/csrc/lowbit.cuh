@@ -136,19 +136,28 @@ __device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
                             *reinterpret_cast<const __half2*>(&c));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+// `one` is the power of two in both halves.  It comes from the kernel's arguments: an instruction has room for one
+// constant, and the compiler, knowing both, would spend a second instruction on each pair of codes.
+constexpr uint32_t kOneF16 = 0x64006400u;   // 1024
+constexpr uint32_t kOneBf16 = 0x43004300u;  // 128
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t b) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(mask), "r"(b));
+  return r;
+}
 // fp16 pair of the 4-bit codes in bits 0-3 of each half (and with kHigh in bits 4-7).
 template <bool kHigh>
-__device__ __forceinline__ uint32_t nibbles_f16(uint32_t w) {
-  if (kHigh) return h2_fma((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u /* 1/16 */, 0xD480D480u /* -72 */);
-  return h2_sub((w & 0x000F000Fu) | 0x64006400u, 0x64086408u /* 1032 */);
+__device__ __forceinline__ uint32_t nibbles_f16(uint32_t w, uint32_t one) {
+  if (kHigh) return h2_fma(and_or(w, 0x00F000F0u, one), 0x2C002C00u /* 1/16 */, 0xD480D480u /* -72 */);
+  return h2_sub(and_or(w, 0x000F000Fu, one), 0x64086408u /* 1032 */);
 }
 // fp16 pair of the 8-bit codes in the bytes of x that `sel` names (0-3), as __byte_perm selectors 0x4y4x.
-__device__ __forceinline__ uint32_t bytes_f16(uint32_t x, uint32_t sel) {
-  return h2_sub(__byte_perm(x, 0x64646464u, sel), 0x64806480u /* 1152 */);
+__device__ __forceinline__ uint32_t bytes_f16(uint32_t x, uint32_t sel, uint32_t one) {
+  return h2_sub(__byte_perm(x, one, sel), 0x64806480u /* 1152 */);
 }
 // bf16 pair of the 4-bit codes in bits 0-3 of each half.
-__device__ __forceinline__ uint32_t nibbles_bf16(uint32_t w) {
-  const uint32_t v = (w & 0x000F000Fu) | 0x43004300u;
+__device__ __forceinline__ uint32_t nibbles_bf16(uint32_t w, uint32_t one) {
+  const uint32_t v = and_or(w, 0x000F000Fu, one);
   const uint32_t k = 0x43084308u;  // 136
   const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&k));
   return *reinterpret_cast<const uint32_t*>(&r);

@@ -180,14 +180,14 @@ struct MatvecArgs {
   const float* steps;
   int64_t lds;
   int64_t K, N;
-  int group;
   const void* X;
   int64_t ldx;
   int64_t M;
   void* Y;
   int64_t ldy;
   int y_bf16;
-  int aligned;  // rows of X may be read 16 bytes at a time
+  int aligned;   // bytes at which every row of X begins a multiple: 16, 4 or 2
+  uint32_t one;  // kOneBf16
 };
 
 constexpr int kTokens = 16;  // tokens of a CTA
@@ -209,7 +209,7 @@ struct MvShape {
   static constexpr int kSmem = kMvWarps * kStages * kStage + kRed;
 };
 
-template <typename T, int kTiles, int kR>
+template <typename T, int kGroup, int kTiles, int kR>
 __global__ void __launch_bounds__(kMvWarps * 32, kTiles * kR <= 2 ? 2 : 1) k_w4_matvec(const __grid_constant__ MatvecArgs a) {
   using S = MvShape<T, kTiles, kR>;
   constexpr int kStages = S::kStages, kPer16 = 16 / sizeof(T);
@@ -221,56 +221,85 @@ __global__ void __launch_bounds__(kMvWarps * 32, kTiles * kR <= 2 ? 2 : 1) k_w4_
   const int tokens = (int)min((int64_t)kTokens, a.M - m0);
   const int sets = (N + 16 * kR - 1) / (16 * kR);
   const int per_set = (nb - warp + kMvWarps - 1) / kMvWarps;  // this warp's blocks of a set (0 for K below its first)
-  const int groups = (K + a.group - 1) / a.group, per_block = kBlock / a.group;
+  const int groups = (K + kGroup - 1) / kGroup;
+  constexpr int kPerBlock = kBlock / kGroup;
   uint8_t* const mine = smem + warp * kStages * S::kStage;
 
-  const T* xp[S::kTok];
+  // Columns without a token hold what lies in shared memory: a column's sums depend on no other column, and theirs are
+  // not stored.
+  const T* xp[S::kTok];  // this lane's first entry
   bool has[S::kTok];
 #pragma unroll
   for (int t = 0; t < S::kTok; ++t) {
     const int tok = S::kPacked ? g / 3 : 8 * t + g;
     has[t] = tok < tokens;
-    xp[t] = static_cast<const T*>(a.X) + (m0 + (has[t] ? tok : 0)) * a.ldx;
+    xp[t] = static_cast<const T*>(a.X) + (m0 + (has[t] ? tok : 0)) * a.ldx + 8 * c;
   }
-  // columns without a token stay zero
-  for (int i = lane; i < kStages * S::kStage / 16; i += 32) reinterpret_cast<uint4*>(mine)[i] = make_uint4(0u, 0u, 0u, 0u);
 
-  // the next block to copy: set, its block, ring stage
-  int set_in = blockIdx.x, block_in = 0, stage_in = 0;
+  // the next block to copy: set, its block, ring stage, and where the set's rows lie
+  int set_in = blockIdx.x, kb_in = warp, stage_in = 0;
+  const uint8_t* code_row[2 * kR];
+  const float* step_row[2 * kR];
+  auto open_set = [&]() {
+#pragma unroll
+    for (int r = 0; r < 2 * kR; ++r) {
+      // rows behind the last one read the last one; their sums are not stored
+      const int64_t n = min((int64_t)set_in * 16 * kR + 8 * r + g, (int64_t)N - 1);
+      code_row[r] = a.codes + n * a.ldc + 16 * c;
+      step_row[r] = a.steps + n * a.lds + c;
+    }
+  };
+  open_set();
   auto issue = [&]() {
     if (set_in < sets && per_set > 0) {
-      const int kb = warp + block_in * kMvWarps;
       uint8_t* const to = mine + stage_in * S::kStage;
-      const uint32_t dst = smem_addr(to) + lane * 16;
+      const uint32_t dst = smem_addr(to) + lane * 16, dst4 = smem_addr(to) + (2 * kR + S::kXPieces) * 512 + lane * 4;
+      const bool steps_on = c < kPerBlock && kb_in * kPerBlock + c < groups;
 #pragma unroll
       for (int r = 0; r < 2 * kR; ++r) {
-        // rows behind the last one read the last one; their sums are not stored
-        const int64_t n = min((int64_t)set_in * 16 * kR + 8 * r + g, (int64_t)N - 1);
-        cp_async<16>(dst + r * 512, a.codes + n * a.ldc + kb * kBlockBytes + 16 * c);
-        const int gi = kb * per_block + c;
-        if (c < per_block && gi < groups)
-          cp_async<4>(smem_addr(to) + (2 * kR + S::kXPieces) * 512 + r * 128 + lane * 4, a.steps + n * a.lds + gi);
+        cp_async<16>(dst + r * 512, code_row[r] + kb_in * kBlockBytes);
+        if (steps_on) cp_async<4>(dst4 + r * 128, step_row[r] + kb_in * kPerBlock);
       }
+      const int k0 = kb_in * kBlock;
+      constexpr int kPieces = 8 / kPer16;  // of eight entries
+      if (a.aligned == 16 && k0 + kBlock <= K) {
 #pragma unroll
-      for (int t = 0; t < S::kTok; ++t)
-        if (has[t]) {
+        for (int t = 0; t < S::kTok; ++t)
+          if (has[t]) {
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const int k0 = kb * kBlock + 32 * h + 8 * c;
-            constexpr int kPieces = 8 / kPer16;  // of eight entries
-            const int at = 2 * kR + (t * 4 + h) * kPieces;
-            if (a.aligned && k0 + 8 <= K) {
+            for (int h = 0; h < 4; ++h)
 #pragma unroll
-              for (int q = 0; q < kPieces; ++q) cp_async<16>(dst + (at + q) * 512, xp[t] + k0 + q * kPer16);
-            } else {
+              for (int q = 0; q < kPieces; ++q)
+                cp_async<16>(dst + (2 * kR + (t * 4 + h) * kPieces + q) * 512, xp[t] + k0 + 32 * h + q * kPer16);
+          }
+      } else {  // the end of a row, or rows that begin anywhere: four bytes at a time, or an entry
+#pragma unroll 1
+        for (int h = 0; h < 4 * S::kTok; ++h) {
+          const int t = h / 4, k = k0 + 32 * (h % 4);
+          if (!(t ? has[S::kTok - 1] : has[0])) continue;
+          const T* const p = (t ? xp[S::kTok - 1] : xp[0]) + k;
+          const int left = (K - k - 8 * c) * (int)sizeof(T);  // bytes of the row
+          const uint32_t slot = dst + (2 * kR + h * kPieces) * 512;
+          if (a.aligned >= 4) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                reinterpret_cast<T*>(to + (at + e / kPer16) * 512 + lane * 16)[e % kPer16] = k0 + e < K ? xp[t][k0 + e] : from_f32<T>(0.f);
+            for (int e = 0; e < 2 * (int)sizeof(T); ++e) {
+              const int n = min(max(left - 4 * e, 0), 4);
+              cp_async_part<4>(slot + e / 4 * 512 + e % 4 * 4, n ? reinterpret_cast<const uint8_t*>(p) + 4 * e : reinterpret_cast<const uint8_t*>(a.codes), n);
             }
+          } else {
+            T* const at = reinterpret_cast<T*>(to + (2 * kR + h * kPieces) * 512 + lane * 16);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              at[e / kPer16 * (512 / sizeof(T)) + e % kPer16] = e * (int)sizeof(T) < left ? p[e] : from_f32<T>(0.f);
           }
         }
+      }
       stage_in = stage_in + 1 == kStages ? 0 : stage_in + 1;
-      if (++block_in == per_set) block_in = 0, set_in += gridDim.x;
+      kb_in += kMvWarps;
+      if (kb_in >= nb) {
+        kb_in = warp, set_in += gridDim.x;
+        open_set();
+      }
     }
     cp_async_commit();
   };
@@ -292,7 +321,6 @@ __global__ void __launch_bounds__(kMvWarps * 32, kTiles * kR <= 2 ? 2 : 1) k_w4_
         for (int j = 0; j < 2; ++j) v[r][j] = *reinterpret_cast<const uint4*>(from + (2 * r + j) * 512 + lane * 16);
       const float* const st = reinterpret_cast<const float*>(from + (2 * kR + S::kXPieces) * 512);
       float acc[kR][kTiles][4];
-      int gi = 0;
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         // the other operand: per tile, the pairs of this half's first four inputs and of its second four
@@ -329,14 +357,14 @@ __global__ void __launch_bounds__(kMvWarps * 32, kTiles * kR <= 2 ? 2 : 1) k_w4_
             }
           }
         }
-        const bool opens = h * 32 % a.group == 0, closes = (h + 1) * 32 % a.group == 0;
+        const bool opens = h * 32 % kGroup == 0, closes = (h + 1) * 32 % kGroup == 0;
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
           const uint32_t p0 = h == 0 ? v[r][0].x : h == 1 ? v[r][0].y : h == 2 ? v[r][0].z : v[r][0].w;
           const uint32_t p1 = h == 0 ? v[r][1].x : h == 1 ? v[r][1].y : h == 2 ? v[r][1].z : v[r][1].w;
           uint32_t q0[4], q1[4];
 #pragma unroll
-          for (int i4 = 0; i4 < 4; ++i4) q0[i4] = nibbles_bf16(p0 >> (4 * i4)), q1[i4] = nibbles_bf16(p1 >> (4 * i4));
+          for (int i4 = 0; i4 < 4; ++i4) q0[i4] = nibbles_bf16(p0 >> (4 * i4), a.one), q1[i4] = nibbles_bf16(p1 >> (4 * i4), a.one);
 #pragma unroll
           for (int t = 0; t < kTiles; ++t) {
             if (opens) acc[r][t][0] = acc[r][t][1] = acc[r][t][2] = acc[r][t][3] = 0.f;
@@ -344,6 +372,7 @@ __global__ void __launch_bounds__(kMvWarps * 32, kTiles * kR <= 2 ? 2 : 1) k_w4_
             mma_bf16(acc[r][t], q0[2], q1[2], q0[3], q1[3], x[t][2], x[t][3]);
           }
           if (closes) {
+            const int gi = h * 32 / kGroup;
             const float d0 = st[(2 * r) * 32 + g * 4 + gi], d1 = st[(2 * r + 1) * 32 + g * 4 + gi];
 #pragma unroll
             for (int t = 0; t < kTiles; ++t) {
@@ -352,7 +381,6 @@ __global__ void __launch_bounds__(kMvWarps * 32, kTiles * kR <= 2 ? 2 : 1) k_w4_
             }
           }
         }
-        if (closes) ++gi;
       }
     }
     // ---- the warps' sums of this set
@@ -387,10 +415,10 @@ __global__ void __launch_bounds__(kMvWarps * 32, kTiles * kR <= 2 ? 2 : 1) k_w4_
   cp_async_wait<0>();
 }
 
-template <typename T, int kTiles, int kR>
+template <typename T, int kGroup, int kTiles, int kR>
 imq_status matvec_shape(const MatvecArgs& a, int num_sms, cudaStream_t st) {
   constexpr int kSmem = MvShape<T, kTiles, kR>::kSmem;
-  const void* fn = reinterpret_cast<const void*>(&k_w4_matvec<T, kTiles, kR>);
+  const void* fn = reinterpret_cast<const void*>(&k_w4_matvec<T, kGroup, kTiles, kR>);
   static std::atomic<int> resident[64];  // CTAs an SM holds, per device; 0: not asked yet
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return IMQ_ERR_CUDA;
@@ -402,19 +430,42 @@ imq_status matvec_shape(const MatvecArgs& a, int num_sms, cudaStream_t st) {
   }
   const int64_t sets = (a.N + 16 * kR - 1) / (16 * kR), most = (int64_t)per_sm * num_sms;
   const dim3 grid((unsigned)(sets < most ? sets : most), (unsigned)((a.M + kTokens - 1) / kTokens));
-  k_w4_matvec<T, kTiles, kR><<<grid, kMvWarps * 32, kSmem, st>>>(a);
+  k_w4_matvec<T, kGroup, kTiles, kR><<<grid, kMvWarps * 32, kSmem, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? IMQ_OK : IMQ_ERR_CUDA;
 }
 
 // Two sets of 16 channels at a time where there are enough of them for every SM: X is read and cut up half as often.
-template <typename T, int kTiles>
+template <typename T, int kGroup, int kTiles>
 imq_status matvec_rows(const MatvecArgs& a, int num_sms, cudaStream_t st) {
-  return a.N > 32 * num_sms ? matvec_shape<T, kTiles, 2>(a, num_sms, st) : matvec_shape<T, kTiles, 1>(a, num_sms, st);
+  return a.N > 32 * num_sms ? matvec_shape<T, kGroup, kTiles, 2>(a, num_sms, st) : matvec_shape<T, kGroup, kTiles, 1>(a, num_sms, st);
+}
+
+template <typename T, int kGroup>
+imq_status matvec_tokens(const MatvecArgs& a, int num_sms, cudaStream_t st) {
+  const int64_t tokens = a.M < kTokens ? a.M : kTokens;
+  if constexpr (sizeof(T) == 2)
+    return tokens <= 8 ? matvec_rows<T, kGroup, 1>(a, num_sms, st) : matvec_rows<T, kGroup, 2>(a, num_sms, st);
+  else
+    return tokens <= 2   ? matvec_rows<T, kGroup, 1>(a, num_sms, st)
+           : tokens <= 8 ? matvec_rows<T, kGroup, 3>(a, num_sms, st)
+                         : matvec_rows<T, kGroup, 6>(a, num_sms, st);
+}
+
+template <typename T>
+imq_status matvec_group(const MatvecArgs& a, int group, int num_sms, cudaStream_t st) {
+  return group == 32   ? matvec_tokens<T, 32>(a, num_sms, st)
+         : group == 64 ? matvec_tokens<T, 64>(a, num_sms, st)
+                       : matvec_tokens<T, 128>(a, num_sms, st);
 }
 
 bool is_float(imq_dtype t) { return t == IMQ_F32 || t == IMQ_BF16; }
 int size_of(imq_dtype t) { return t == IMQ_F32 ? 4 : 2; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+int row_alignment(const void* p, int64_t row_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(p) | (uintptr_t)row_bytes;
+  return x % 16 == 0 ? 16 : x % 4 == 0 ? 4 : 2;
+}
 
 // What every call on a 4-bit weight checks.
 imq_status check_weight(const void* codes, int64_t ldc, const void* steps, int64_t lds, int64_t K, int64_t N, int32_t group) {
@@ -500,14 +551,9 @@ imq_status launch_w4_matvec(const uint8_t* codes, int64_t ldc, const float* step
   DeviceState* ds;
   s = device_state(&ds);
   if (s != IMQ_OK) return s;
-  MatvecArgs a{codes, ldc, steps, lds, K, N, group, X, ldx, M, Y, ldy, yt == IMQ_BF16,
-               aligned16(X) && (M == 1 || ldx * size_of(xt) % 16 == 0)};
-  const int64_t tokens = M < kTokens ? M : kTokens;
-  if (xt == IMQ_BF16)
-    return tokens <= 8 ? matvec_rows<__nv_bfloat16, 1>(a, ds->num_sms, st) : matvec_rows<__nv_bfloat16, 2>(a, ds->num_sms, st);
-  return tokens <= 2   ? matvec_rows<float, 1>(a, ds->num_sms, st)
-         : tokens <= 8 ? matvec_rows<float, 3>(a, ds->num_sms, st)
-                       : matvec_rows<float, 6>(a, ds->num_sms, st);
+  MatvecArgs a{codes, ldc, steps, lds, K, N, X, ldx, M, Y, ldy, yt == IMQ_BF16,
+               row_alignment(X, M == 1 ? 0 : ldx * size_of(xt)), kOneBf16};
+  return xt == IMQ_BF16 ? matvec_group<__nv_bfloat16>(a, group, ds->num_sms, st) : matvec_group<float>(a, group, ds->num_sms, st);
 }
 
 }  // namespace imq
