@@ -18,7 +18,30 @@ struct VecArgs {
   const int64_t* slots;
   int aligned;
   int32_t* status;
+  uint32_t one;  // kOneF16
 };
+
+// Tokens a lane group takes: their loads are under way together.
+constexpr int kTokens = 2;
+
+// The cache place of a token's vector: page, and vector within the page's head block.  False for a token that is skipped.
+__device__ __forceinline__ bool locate(const VecArgs& a, int64_t tok, int head, bool report, uint32_t* page, int64_t* at) {
+  const int64_t slot = tok < a.n ? a.slots[tok] : -1;
+  if (slot < 0) return false;
+  if (slot >= a.c.n_pages * a.c.page_size) {
+    if (report) set_status(a.status, IMQ_ERR_BOUNDS);
+    return false;
+  }
+  uint32_t p, place;
+  if (slot <= UINT32_MAX) {
+    p = (uint32_t)slot / (uint32_t)a.c.page_size, place = (uint32_t)slot - p * (uint32_t)a.c.page_size;
+  } else {
+    p = (uint32_t)(slot / a.c.page_size), place = (uint32_t)(slot % a.c.page_size);
+  }
+  *page = p;
+  *at = head * (int64_t)a.c.page_size + place;
+  return true;
+}
 
 template <typename T>
 __device__ __forceinline__ void load_vec(const T* p, bool vec, float (&x)[8]) {
@@ -29,106 +52,141 @@ __device__ __forceinline__ void load_vec(const T* p, bool vec, float (&x)[8]) {
     for (int e = 0; e < 8; ++e) x[e] = to_f32(p[e]);
   }
 }
-template <typename T>
-__device__ __forceinline__ void store_vec(T* p, bool vec, const float (&x)[8]) {
+// 16 bytes.
+__device__ __forceinline__ void store_vec(__nv_bfloat16* p, bool vec, const float (&x)[8]) {
   if (vec) {
     store8(p, x);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) p[e] = from_f32<T>(x[e]);
+    for (int e = 0; e < 8; ++e) p[e] = from_f32<__nv_bfloat16>(x[e]);
+  }
+}
+__device__ __forceinline__ void store_vec(float* p, bool vec, const float (&x)[4]) {
+  if (vec) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[e] = x[e];
   }
 }
 
 // kLanes: lanes of a vector's group (a power of two >= D / 8; the lanes at and above D / 8 hold zeros).
 template <typename T, int kBits, int kLanes>
-__global__ void __launch_bounds__(256) k_kv_write(VecArgs a) {
-  constexpr int kBytes = kBits;  // bytes of 8 codes
+__global__ void __launch_bounds__(256) k_kv_write(const __grid_constant__ VecArgs a) {
   const imq_kv_cache& c = a.c;
-  const int i = threadIdx.x % kLanes;
-  const int64_t unit = (int64_t)blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
-  const int64_t tok = unit / c.n_heads;
-  const int head = (int)(unit - tok * c.n_heads);
-  const int64_t slot = tok < a.n ? a.slots[tok] : -1;
-  const bool inside = slot >= 0 && slot < c.n_pages * c.page_size;
-  if (slot >= 0 && !inside && i == 0) set_status(a.status, IMQ_ERR_BOUNDS);
-  const bool lane = inside && 8 * i < c.head_dim;
-  float k[8] = {}, v[8] = {};
-  if (lane) {
-    load_vec(static_cast<const T*>(a.K) + tok * a.k_tok + head * a.k_head + 8 * i, a.aligned, k);
-    load_vec(static_cast<const T*>(a.V) + tok * a.v_tok + head * a.v_head + 8 * i, a.aligned, v);
-  }
-  uint32_t kk = 0, vk = 0;
+  const int i = threadIdx.x % kLanes, vec_bytes = c.head_dim * kBits / 8;
+  const uint32_t unit = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
+  const int64_t tok0 = (int64_t)(unit / (uint32_t)c.n_heads) * kTokens;
+  const int head = unit % (uint32_t)c.n_heads;
+  const bool lane = 8 * i < c.head_dim;
+  float k[kTokens][8] = {}, v[kTokens][8] = {};
+  uint32_t page[kTokens];
+  int64_t at[kTokens];
+  bool on[kTokens];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) kk = max(kk, abs_key(k[e])), vk = max(vk, abs_key(v[e]));
+  for (int j = 0; j < kTokens; ++j)
+    if (lane && tok0 + j < a.n) {
+      load_vec(static_cast<const T*>(a.K) + (tok0 + j) * a.k_tok + head * a.k_head + 8 * i, a.aligned, k[j]);
+      load_vec(static_cast<const T*>(a.V) + (tok0 + j) * a.v_tok + head * a.v_head + 8 * i, a.aligned, v[j]);
+    }
 #pragma unroll
-  for (int o = 1; o < kLanes; o <<= 1) {
-    kk = max(kk, __shfl_xor_sync(0xffffffffu, kk, o));
-    vk = max(vk, __shfl_xor_sync(0xffffffffu, vk, o));
-  }
-  if (!lane) return;
-  constexpr float kBeta = (float)((1 << (kBits - 1)) - 1);
-  constexpr uint32_t kBias = 1u << (kBits - 1);
-  float ks, vs, kd, vd;
-  group_scale(kk, kBeta, &ks, &kd);
-  group_scale(vk, kBeta, &vs, &vd);
-  uint32_t ku[8], vu[8];
+  for (int j = 0; j < kTokens; ++j) on[j] = locate(a, tok0 + j, head, i == 0, &page[j], &at[j]);
+  uint32_t key[4] = {};  // of the first token's key and value, and the second's
 #pragma unroll
-  for (int e = 0; e < 8; ++e) ku[e] = code_of(k[e], ks, kBias), vu[e] = code_of(v[e], vs, kBias);
-  const int64_t page = slot / c.page_size, at = head * (int64_t)c.page_size + (slot - page * c.page_size);
-  uint8_t* kp = c.k + page * c.k_page_stride + at * (c.head_dim * kBits / 8) + kBytes * i;
-  uint8_t* vp = c.v + page * c.v_page_stride + at * (c.head_dim * kBits / 8) + kBytes * i;
-  if constexpr (kBits == 4) {
-    *reinterpret_cast<uint32_t*>(kp) = pack_nibbles(ku);
-    *reinterpret_cast<uint32_t*>(vp) = pack_nibbles(vu);
-  } else {
-    *reinterpret_cast<uint2*>(kp) = make_uint2(ku[0] | ku[1] << 8 | ku[2] << 16 | ku[3] << 24,
-                                               ku[4] | ku[5] << 8 | ku[6] << 16 | ku[7] << 24);
-    *reinterpret_cast<uint2*>(vp) = make_uint2(vu[0] | vu[1] << 8 | vu[2] << 16 | vu[3] << 24,
-                                               vu[4] | vu[5] << 8 | vu[6] << 16 | vu[7] << 24);
-  }
-  if (i == 0) {
-    *reinterpret_cast<float2*>(c.steps + page * c.steps_page_stride + at * 2) = make_float2(kd, vd);
-    if (!key_finite(kk) || !key_finite(vk)) set_status(a.status, IMQ_ERR_NONFINITE);
+  for (int j = 0; j < kTokens; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      key[2 * j] = max(key[2 * j], abs_key(k[j][e]));
+      key[2 * j + 1] = max(key[2 * j + 1], abs_key(v[j][e]));
+    }
+#pragma unroll
+  for (int o = 1; o < kLanes; o <<= 1)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) key[q] = max(key[q], __shfl_xor_sync(0xffffffffu, key[q], o));
+  float s[4], step[4];
+  four_scales(key, (float)((1 << (kBits - 1)) - 1), s, step);
+#pragma unroll
+  for (int j = 0; j < kTokens; ++j) {
+    if (!lane || !on[j]) continue;
+    uint8_t* kp = c.k + page[j] * c.k_page_stride + at[j] * vec_bytes + kBits * i;  // eight codes are kBits bytes
+    uint8_t* vp = c.v + page[j] * c.v_page_stride + at[j] * vec_bytes + kBits * i;
+    const float ks = s[2 * j], vs = s[2 * j + 1];
+    if constexpr (kBits == 4) {
+      *reinterpret_cast<uint32_t*>(kp) = pack4(k[j], ks);
+      *reinterpret_cast<uint32_t*>(vp) = pack4(v[j], vs);
+    } else {
+      *reinterpret_cast<uint2*>(kp) = make_uint2(pack8(k[j][0], k[j][1], k[j][2], k[j][3], ks), pack8(k[j][4], k[j][5], k[j][6], k[j][7], ks));
+      *reinterpret_cast<uint2*>(vp) = make_uint2(pack8(v[j][0], v[j][1], v[j][2], v[j][3], vs), pack8(v[j][4], v[j][5], v[j][6], v[j][7], vs));
+    }
+    if (i == 0) {
+      *reinterpret_cast<float2*>(c.steps + page[j] * c.steps_page_stride + at[j] * 2) = make_float2(step[2 * j], step[2 * j + 1]);
+      if (!key_finite(key[2 * j]) || !key_finite(key[2 * j + 1])) set_status(a.status, IMQ_ERR_NONFINITE);
+    }
   }
 }
 
+// A lane makes 16 bytes of a vector: 8 entries of bf16, 4 of fp32 (so that a warp's stores are one piece).  kLanes: a power
+// of two that covers a vector.
 template <typename T, int kBits, int kLanes>
-__global__ void __launch_bounds__(256) k_kv_read(VecArgs a) {
-  constexpr int kBytes = kBits;
+__global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ VecArgs a) {
+  constexpr int kMine = 16 / sizeof(T), kWords = kMine * kBits > 32 ? 2 : 1;
   const imq_kv_cache& c = a.c;
-  const int i = threadIdx.x % kLanes;
-  const int64_t unit = (int64_t)blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
-  const int64_t tok = unit / c.n_heads;
-  const int head = (int)(unit - tok * c.n_heads);
-  const int64_t slot = tok < a.n ? a.slots[tok] : -1;
-  const bool inside = slot >= 0 && slot < c.n_pages * c.page_size;
-  if (slot >= 0 && !inside && i == 0) set_status(a.status, IMQ_ERR_BOUNDS);
-  if (!inside || 8 * i >= c.head_dim) return;
-  const int64_t page = slot / c.page_size, at = head * (int64_t)c.page_size + (slot - page * c.page_size);
-  const uint8_t* kp = c.k + page * c.k_page_stride + at * (c.head_dim * kBits / 8) + kBytes * i;
-  const uint8_t* vp = c.v + page * c.v_page_stride + at * (c.head_dim * kBits / 8) + kBytes * i;
-  const float2 step = *reinterpret_cast<const float2*>(c.steps + page * c.steps_page_stride + at * 2);
-  float k[8], v[8];
-  if constexpr (kBits == 4) {
-    const uint32_t kw = *reinterpret_cast<const uint32_t*>(kp), vw = *reinterpret_cast<const uint32_t*>(vp);
+  const int i = threadIdx.x % kLanes, vec_bytes = c.head_dim * kBits / 8;
+  const uint32_t unit = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
+  const int64_t tok0 = (int64_t)(unit / (uint32_t)c.n_heads) * kTokens;
+  const int head = unit % (uint32_t)c.n_heads;
+  // the word (or two) of this lane's codes; at 4 bits and fp32 two lanes share a word
+  const int from = i * kMine * kBits / 32 * 4;
+  uint32_t kw[kTokens][kWords], vw[kTokens][kWords];
+  float2 step[kTokens];
+  bool on[kTokens];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) k[e] = __fmul_rn(nibble_value(kw, e), step.x), v[e] = __fmul_rn(nibble_value(vw, e), step.y);
-  } else {
-    const uint2 kw = *reinterpret_cast<const uint2*>(kp), vw = *reinterpret_cast<const uint2*>(vp);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t ku = ((e < 4 ? kw.x : kw.y) >> (8 * (e & 3))) & 255u, vu = ((e < 4 ? vw.x : vw.y) >> (8 * (e & 3))) & 255u;
-      k[e] = __fmul_rn((float)ku - 128.f, step.x), v[e] = __fmul_rn((float)vu - 128.f, step.y);
+  for (int j = 0; j < kTokens; ++j) {
+    uint32_t page;
+    int64_t at;
+    on[j] = locate(a, tok0 + j, head, i == 0, &page, &at) && kMine * i < c.head_dim;
+    if (!on[j]) continue;
+    const uint8_t* kp = c.k + page * c.k_page_stride + at * vec_bytes + from;
+    const uint8_t* vp = c.v + page * c.v_page_stride + at * vec_bytes + from;
+    step[j] = *reinterpret_cast<const float2*>(c.steps + page * c.steps_page_stride + at * 2);
+    if constexpr (kWords == 2) {
+      const uint2 x = *reinterpret_cast<const uint2*>(kp), y = *reinterpret_cast<const uint2*>(vp);
+      kw[j][0] = x.x, kw[j][1] = x.y, vw[j][0] = y.x, vw[j][1] = y.y;
+    } else {
+      kw[j][0] = *reinterpret_cast<const uint32_t*>(kp), vw[j][0] = *reinterpret_cast<const uint32_t*>(vp);
     }
   }
-  if (a.K) store_vec(static_cast<T*>(a.K) + tok * a.k_tok + head * a.k_head + 8 * i, a.aligned, k);
-  if (a.V) store_vec(static_cast<T*>(a.V) + tok * a.v_tok + head * a.v_head + 8 * i, a.aligned, v);
+  auto values = [&](const uint32_t(&w)[kWords], float s, float(&x)[kMine]) {
+#pragma unroll
+    for (int q = 0; q < kMine / 2; ++q) {
+      float2 v;
+      if constexpr (kBits == 8) v = byte_pair(w[q / 2], q % 2, a.one);
+      else if constexpr (kMine == 8) v = nibble_pair(w[0], q, a.one);
+      else v = nibble_pair(i & 1 ? w[0] >> 8 : w[0], q, a.one);  // codes 4-7 lie 8 bits above codes 0-3
+      x[2 * q] = __fmul_rn(v.x, s), x[2 * q + 1] = __fmul_rn(v.y, s);
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < kTokens; ++j) {
+    if (!on[j]) continue;
+    float x[kMine];
+    if (a.K) {
+      values(kw[j], step[j].x, x);
+      store_vec(static_cast<T*>(a.K) + (tok0 + j) * a.k_tok + head * a.k_head + kMine * i, a.aligned, x);
+    }
+    if (a.V) {
+      values(vw[j], step[j].y, x);
+      store_vec(static_cast<T*>(a.V) + (tok0 + j) * a.v_tok + head * a.v_head + kMine * i, a.aligned, x);
+    }
+  }
 }
 
 template <typename T, int kBits>
 void run(bool write, const VecArgs& a, cudaStream_t st) {
-  const int lanes = a.c.head_dim <= 64 ? 8 : a.c.head_dim <= 128 ? 16 : 32;
-  const unsigned ctas = (unsigned)((a.n * a.c.n_heads + 256 / lanes - 1) / (256 / lanes));
+  const int mine = write ? 8 : 16 / (int)sizeof(T), need = a.c.head_dim / mine;
+  const int lanes = need <= 8 ? 8 : need <= 16 ? 16 : need <= 32 ? 32 : 64;
+  const int64_t units = (a.n + kTokens - 1) / kTokens * a.c.n_heads;
+  const unsigned ctas = (unsigned)((units + 256 / lanes - 1) / (256 / lanes));
   if (write) {
     if (lanes == 8) k_kv_write<T, kBits, 8><<<ctas, 256, 0, st>>>(a);
     if (lanes == 16) k_kv_write<T, kBits, 16><<<ctas, 256, 0, st>>>(a);
@@ -137,6 +195,7 @@ void run(bool write, const VecArgs& a, cudaStream_t st) {
     if (lanes == 8) k_kv_read<T, kBits, 8><<<ctas, 256, 0, st>>>(a);
     if (lanes == 16) k_kv_read<T, kBits, 16><<<ctas, 256, 0, st>>>(a);
     if (lanes == 32) k_kv_read<T, kBits, 32><<<ctas, 256, 0, st>>>(a);
+    if (lanes == 64) k_kv_read<T, kBits, 64><<<ctas, 256, 0, st>>>(a);
   }
 }
 
@@ -151,12 +210,12 @@ imq_status launch(bool write, const imq_kv_cache* cache, void* K, int64_t k_tok,
   const uintptr_t kp = reinterpret_cast<uintptr_t>(K), vp = reinterpret_cast<uintptr_t>(V);
   if (!slots || (write && (!K || !V)) || (!K && !V) || ((kp | vp) & (size - 1)) || (reinterpret_cast<uintptr_t>(slots) & 7))
     return IMQ_ERR_ARG;
-  if (n > (int64_t)INT32_MAX * 8 / cache->n_heads) return IMQ_ERR_UNSUPPORTED;
+  if (n > INT32_MAX / cache->n_heads) return IMQ_ERR_UNSUPPORTED;
   DeviceState* ds;
   s = device_state(&ds);
   if (s != IMQ_OK) return s;
   const int64_t strides = ((K ? k_tok | k_head : 0) | (V ? v_tok | v_head : 0)) * size;
-  VecArgs a{*cache, K, V, n, k_tok, k_head, v_tok, v_head, slots, ((kp | vp | (uintptr_t)strides) & 15) == 0, ds->status};
+  VecArgs a{*cache, K, V, n, k_tok, k_head, v_tok, v_head, slots, ((kp | vp | (uintptr_t)strides) & 15) == 0, ds->status, kOneF16};
   if (t == IMQ_F32) {
     if (cache->bits == 4) run<float, 4>(write, a, st);
     else run<float, 8>(write, a, st);

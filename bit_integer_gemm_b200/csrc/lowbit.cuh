@@ -31,24 +31,39 @@ __device__ __forceinline__ void group_scale(uint32_t key, float beta, float* s, 
   if (q == 0.f || !key_finite(__float_as_uint(*s))) *s = *step = 1.f;
 }
 
-// round_half_even(fp32(x * s)) + bias for |x * s| <= 128: adding 1.5 * 2^23 rounds to an integer in the low
-// mantissa bits.  (|x| <= q, so |fp32(x * s)| is at most beta but for the rounding of s, well below beta + 1/2.)
-// s = 0 marks a non-finite group, whose codes are 0 whatever x is.
-__device__ __forceinline__ uint32_t code_of(float x, float s, uint32_t bias) {
-  if (s == 0.f) return bias;
-  return (__float_as_uint(__fadd_rn(__fmul_rn(x, s), 12582912.f)) + bias) & 0xFFu;
+// Four different groups' scales with one division each way instead of four: every lane of four works out one group's
+// and hands it to the others.  All lanes of an aligned quad hold the same four keys.
+__device__ __forceinline__ void four_scales(const uint32_t (&key)[4], float beta, float (&s)[4], float (&step)[4]) {
+  const int j = threadIdx.x & 3;
+  float one_s, one_step;
+  group_scale(j < 2 ? (j == 0 ? key[0] : key[1]) : (j == 2 ? key[2] : key[3]), beta, &one_s, &one_step);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s[i] = __shfl_sync(0xffffffffu, one_s, i, 4);
+    step[i] = __shfl_sync(0xffffffffu, one_step, i, 4);
+  }
 }
 
-// Eight 4-bit codes in a word: code e in bits 4 * (e / 2 + 4 * (e % 2)), so that one mask leaves the codes
-// 2i and 2i + 1 in the two halves of a register.
-__device__ __forceinline__ uint32_t pack_nibbles(const uint32_t (&u)[8]) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) w |= u[e] << (4 * (e / 2 + 4 * (e % 2)));
-  return w;
+// A code in the low bits of a float: round_half_even(fp32(x * s)) + bias on top of 0x4B400000, for |x * s| <= 128 and
+// an even bias.  (Adding 1.5 * 2^23 rounds to an integer in the low mantissa bits; |x| <= q, so |fp32(x * s)| is at
+// most beta but for the rounding of s, well below beta + 1/2.)
+__device__ __forceinline__ uint32_t code_bits(float x, float s, float bias) {
+  return __float_as_uint(__fadd_rn(__fmul_rn(x, s), 12582912.f + bias));
 }
-__device__ __forceinline__ float nibble_value(uint32_t w, int e) {
-  return (float)(int32_t)((w >> (4 * (e / 2 + 4 * (e % 2)))) & 15u) - 8.f;
+// Eight 4-bit codes in a word: code e in bits 4 * (e / 2 + 4 * (e % 2)), so that one mask leaves the codes 2i and
+// 2i + 1 in the two halves of a register.  The codes are added up where they belong, and what the upper bits of
+// their floats add up to is taken off.  s = 0 marks a non-finite group: its codes are 0 whatever x is.
+__device__ __forceinline__ uint32_t pack4(const float (&x)[8], float s) {
+  uint32_t w = 0u - 0x4B400000u * 0x11111111u;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w += code_bits(x[e], s, 8.f) << (4 * (e / 2 + 4 * (e % 2)));
+  return s == 0.f ? 0x88888888u : w;
+}
+// Four 8-bit codes in a word.
+__device__ __forceinline__ uint32_t pack8(float x0, float x1, float x2, float x3, float s) {
+  const uint32_t w = code_bits(x0, s, 128.f) + (code_bits(x1, s, 128.f) << 8) + (code_bits(x2, s, 128.f) << 16) +
+                     (code_bits(x3, s, 128.f) << 24) - 0x4B400000u * 0x01010101u;
+  return s == 0.f ? 0x80808080u : w;
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -154,6 +169,18 @@ __device__ __forceinline__ uint32_t nibbles_f16(uint32_t w, uint32_t one) {
 // fp16 pair of the 8-bit codes in the bytes of x that `sel` names (0-3), as __byte_perm selectors 0x4y4x.
 __device__ __forceinline__ uint32_t bytes_f16(uint32_t x, uint32_t sel, uint32_t one) {
   return h2_sub(__byte_perm(x, one, sel), 0x64806480u /* 1152 */);
+}
+// Codes 2i and 2i + 1 of a word of eight 4-bit codes, and bytes i and i + 1 of a word, as fp32.
+__device__ __forceinline__ float2 nibble_pair(uint32_t w, int i, uint32_t one) {
+  const uint32_t h = i == 0   ? nibbles_f16<false>(w, one)
+                     : i == 1 ? nibbles_f16<true>(w, one)
+                     : i == 2 ? nibbles_f16<false>(w >> 8, one)
+                              : nibbles_f16<true>(w >> 8, one);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+__device__ __forceinline__ float2 byte_pair(uint32_t w, int i, uint32_t one) {
+  const uint32_t h = bytes_f16(w, i == 0 ? 0x5150 : 0x5352, one);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 // bf16 pair of the 4-bit codes in bits 0-3 of each half.
 __device__ __forceinline__ uint32_t nibbles_bf16(uint32_t w, uint32_t one) {

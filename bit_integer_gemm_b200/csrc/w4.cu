@@ -26,83 +26,128 @@ struct QuantArgs {
   int64_t ldc;
   float* steps;
   int64_t lds;
-  int group;
-  int aligned;  // rows of W may be read 16 bytes at a time
+  int log_group;
+  int vec;  // rows of W may be read 16 bytes (stored N x K) or two entries (K x N) at a time
   int32_t* status;
 };
 
-// Quantises the 8 entries x of lane's part of a block: `lanes` lanes (4, 8 or 16, aligned) share a group.
-// Returns the packed word; *step is the group's.
-__device__ __forceinline__ uint32_t quantise_word(const float (&x)[8], int lanes, float* step, bool* bad) {
+__device__ __forceinline__ uint32_t max_key(const float (&x)[8]) {
   uint32_t key = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) key = max(key, abs_key(x[e]));
-  for (int o = 1; o < lanes; o <<= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
-  float s;
-  group_scale(key, 7.f, &s, step);
-  *bad = !key_finite(key);
-  uint32_t u[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) u[e] = code_of(x[e], s, 8u) & 15u;
-  return pack_nibbles(u);
+  return key;
 }
 
-// W stored N x K: half a warp takes a block of 128 inputs of one row, 8 inputs a lane.
+// Row kernels (W stored N x K): a warp takes 256 inputs (two blocks) of four rows, 8 inputs of each a lane.
+constexpr int kRows = 4;
+
+// Eight consecutive entries for each lane of the warp, from 256 consecutive ones of a row that begin anywhere: read in
+// order, turned in shared memory (`turn`, 288 floats of the warp's own, a float of padding every 8 entries).
+template <typename T>
+__device__ __forceinline__ void load256(const T* p, int left, float* turn, int lane, float (&x)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = e * 32 + lane < left ? to_f32(p[e * 32 + lane]) : 0.f;
+  __syncwarp();
+#pragma unroll
+  for (int e = 0; e < 8; ++e) turn[e * 36 + lane + lane / 8] = x[e];
+  __syncwarp();
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = turn[9 * lane + e];
+}
+
 template <typename T>
 __global__ void __launch_bounds__(256) k_w4_quantize_rows(QuantArgs a) {
-  const int64_t nb = (a.K + kBlock - 1) / kBlock;
-  const int lane = threadIdx.x & 31, i = lane & 15;
-  const int64_t unit = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * 2 + (lane >> 4);
-  const int64_t total = a.N * nb;
-  const bool live = unit < total;
-  const int64_t n = live ? unit / nb : 0, kb = live ? unit % nb : 0;
-  const int64_t k0 = kb * kBlock + 8 * i;
-  float x[8];
-  if (live && a.aligned && k0 + 8 <= a.K) {
-    load8(static_cast<const T*>(a.W) + n * a.ldw + k0, x);
+  __shared__ float s_turn[8][288];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = lane & 15;
+  const uint32_t per_row = ((uint32_t)a.K + 255) / 256, unit = blockIdx.x * 8 + warp;
+  const int n0 = (int)(unit / per_row) * kRows, k0 = (int)(unit % per_row) * 256, k = k0 + 8 * lane;
+  const int N = (int)a.N, K = (int)a.K;
+  if (n0 >= N) return;
+  const T* const p = static_cast<const T*>(a.W) + n0 * a.ldw + k0;
+  float x[kRows][8];
+  if (a.vec && k0 + 256 <= K) {
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) load8(p + (n0 + j < N ? j : 0) * a.ldw + 8 * lane, x[j]);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      x[e] = live && k0 + e < a.K ? to_f32(static_cast<const T*>(a.W)[n * a.ldw + k0 + e]) : 0.f;
+    for (int j = 0; j < kRows; ++j) load256(p + (n0 + j < N ? j : 0) * a.ldw, K - k0, s_turn[warp], lane, x[j]);
   }
-  float step;
-  bool bad;
-  const uint32_t w = quantise_word(x, a.group / 8, &step, &bad);
-  if (!live) return;
-  reinterpret_cast<uint32_t*>(a.codes + n * a.ldc + kb * kBlockBytes)[word_of(i)] = w;
-  if ((8 * i) % a.group == 0 && k0 < a.K) {
-    a.steps[n * a.lds + k0 / a.group] = step;
-    if (bad) set_status(a.status, IMQ_ERR_NONFINITE);
+  uint32_t key[kRows];
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) key[j] = max_key(x[j]);
+  for (int o = 1; o < 1 << (a.log_group - 3); o <<= 1)
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) key[j] = max(key[j], __shfl_xor_sync(0xffffffffu, key[j], o));
+  float s[kRows], step[kRows];
+  four_scales(key, 7.f, s, step);
+  if (k - 8 * i >= K) return;  // the row's last block was the other half's
+  const bool writes_step = ((8 * i) & ((1 << a.log_group) - 1)) == 0 && k < K;
+  uint8_t* const to = a.codes + n0 * a.ldc + k0 / kBlock * kBlockBytes + (lane >> 4) * kBlockBytes + 4 * word_of(i);
+  float* const to_step = a.steps + n0 * a.lds + (k >> a.log_group);
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    if (n0 + j >= N) break;
+    *reinterpret_cast<uint32_t*>(to + j * a.ldc) = pack4(x[j], s[j]);
+    if (writes_step) {
+      to_step[j * a.lds] = step[j];
+      if (!key_finite(key[j])) set_status(a.status, IMQ_ERR_NONFINITE);
+    }
   }
 }
 
-// W stored K x N: a CTA takes 128 inputs of 32 channels through shared memory.
+// Column kernels (W stored K x N): a CTA takes 128 inputs of 64 channels.  Warp w holds the inputs 8w .. 8w + 7, a lane
+// two channels: what it reads in order is what it packs; only the groups' scales and the packed words cross warps.
+constexpr int kColChannels = 64;
 template <typename T>
-__global__ void __launch_bounds__(256) k_w4_quantize_cols(QuantArgs a) {
-  __shared__ float tile[32][kBlock + 1];
-  const int64_t kb = blockIdx.y, n0 = (int64_t)blockIdx.x * 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int r = warp; r < kBlock; r += 8) {
-    const int64_t k = kb * kBlock + r, n = n0 + lane;
-    tile[lane][r] = k < a.K && n < a.N ? to_f32(static_cast<const T*>(a.W)[k * a.ldw + n]) : 0.f;
+__global__ void __launch_bounds__(512) k_w4_quantize_cols(QuantArgs a) {
+  __shared__ uint32_t s_key[16][kColChannels], s_word[kColChannels][17];
+  __shared__ float s_scale[4][kColChannels];
+  const int k0 = blockIdx.y * kBlock, n0 = blockIdx.x * kColChannels, K = (int)a.K, N = (int)a.N;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = k0 + 8 * warp, n = n0 + 2 * lane;
+  const T* const p = static_cast<const T*>(a.W) + k * a.ldw + n;
+  float x[2][8];
+  if (a.vec && k + 8 <= K && n + 1 < N) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (sizeof(T) == 4) {
+        const float2 v = *reinterpret_cast<const float2*>(p + e * a.ldw);
+        x[0][e] = v.x, x[1][e] = v.y;
+      } else {
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(p + e * a.ldw);
+        x[0][e] = __uint_as_float(v << 16), x[1][e] = __uint_as_float(v & 0xFFFF0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[0][e] = k + e < K && n < N ? to_f32(p[e * a.ldw]) : 0.f;
+      x[1][e] = k + e < K && n + 1 < N ? to_f32(p[e * a.ldw + 1]) : 0.f;
+    }
+  }
+  *reinterpret_cast<uint2*>(&s_key[warp][2 * lane]) = make_uint2(max_key(x[0]), max_key(x[1]));
+  __syncthreads();
+  const int log8 = a.log_group - 3;  // a group is 2^log8 warps
+  if (threadIdx.x < kColChannels << (4 - log8)) {
+    const int c = threadIdx.x % kColChannels, group = threadIdx.x / kColChannels, at = k0 + (group << a.log_group);
+    uint32_t key = 0;
+    for (int o = 0; o < 1 << log8; ++o) key = max(key, s_key[(group << log8) + o][c]);
+    float s, step;
+    group_scale(key, 7.f, &s, &step);
+    s_scale[group][c] = s;
+    if (n0 + c < N && at < K) {
+      a.steps[(n0 + c) * a.lds + (at >> a.log_group)] = step;
+      if (!key_finite(key)) set_status(a.status, IMQ_ERR_NONFINITE);
+    }
   }
   __syncthreads();
-  const int i = lane & 15;
-  const int64_t k0 = kb * kBlock + 8 * i;
-  for (int r = 2 * warp + (lane >> 4); r < 32; r += 16) {
-    float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = tile[r][8 * i + e];
-    float step;
-    bool bad;
-    const uint32_t w = quantise_word(x, a.group / 8, &step, &bad);
-    const int64_t n = n0 + r;
-    if (n >= a.N) continue;
-    reinterpret_cast<uint32_t*>(a.codes + n * a.ldc + kb * kBlockBytes)[word_of(i)] = w;
-    if ((8 * i) % a.group == 0 && k0 < a.K) {
-      a.steps[n * a.lds + k0 / a.group] = step;
-      if (bad) set_status(a.status, IMQ_ERR_NONFINITE);
-    }
+  for (int j = 0; j < 2; ++j) s_word[2 * lane + j][word_of(warp)] = pack4(x[j], s_scale[warp >> log8][2 * lane + j]);
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kColChannels * 16 / 512; ++q) {
+    const int c = threadIdx.x / 16 + 32 * q;
+    if (n0 + c < N)
+      reinterpret_cast<uint32_t*>(a.codes + (n0 + c) * a.ldc + (int64_t)blockIdx.y * kBlockBytes)[threadIdx.x % 16] = s_word[c][threadIdx.x % 16];
   }
 }
 
@@ -112,52 +157,104 @@ struct DequantArgs {
   const float* steps;
   int64_t lds;
   int64_t K, N;
-  int group;
+  int log_group;
   void* W;
   int64_t ldw;
-  int aligned;
+  int vec;
+  uint32_t one;  // kOneF16
 };
 
+__device__ __forceinline__ void word_values(uint32_t w, float step, uint32_t one, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = nibble_pair(w, i, one);
+    x[2 * i] = __fmul_rn(v.x, step), x[2 * i + 1] = __fmul_rn(v.y, step);
+  }
+}
+
+// The row and column kernels of the quantiser the other way round.
 template <typename T>
 __global__ void __launch_bounds__(256) k_w4_dequantize_rows(DequantArgs a) {
-  const int64_t nb = (a.K + kBlock - 1) / kBlock;
-  const int64_t unit = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 4;
-  const int i = threadIdx.x & 15;
-  if (unit >= a.N * nb) return;
-  const int64_t n = unit / nb, kb = unit % nb, k0 = kb * kBlock + 8 * i;
-  if (k0 >= a.K) return;
-  const uint32_t w = reinterpret_cast<const uint32_t*>(a.codes + n * a.ldc + kb * kBlockBytes)[word_of(i)];
-  const float step = a.steps[n * a.lds + k0 / a.group];
-  float x[8];
+  __shared__ float s_turn[8][288];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = lane & 15;
+  const uint32_t per_row = ((uint32_t)a.K + 255) / 256, unit = blockIdx.x * 8 + warp;
+  const int n0 = (int)(unit / per_row) * kRows, k0 = (int)(unit % per_row) * 256, k = k0 + 8 * lane;
+  const int N = (int)a.N, K = (int)a.K;
+  if (n0 >= N) return;
+  const uint8_t* const from = a.codes + n0 * a.ldc + k0 / kBlock * kBlockBytes + (lane >> 4) * kBlockBytes + 4 * word_of(i);
+  const float* const from_step = a.steps + n0 * a.lds + (k >> a.log_group);
+  uint32_t w[kRows];
+  float step[kRows];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(nibble_value(w, e), step);
-  T* out = static_cast<T*>(a.W) + n * a.ldw + k0;
-  if (a.aligned && k0 + 8 <= a.K) {
-    store8(out, x);
-  } else {
-    for (int e = 0; e < 8 && k0 + e < a.K; ++e) out[e] = from_f32<T>(x[e]);
+  for (int j = 0; j < kRows; ++j) {
+    const bool on = n0 + j < N && k < K;
+    w[j] = on ? *reinterpret_cast<const uint32_t*>(from + j * a.ldc) : 0u;
+    step[j] = on ? from_step[j * a.lds] : 0.f;
+  }
+  T* const out = static_cast<T*>(a.W) + n0 * a.ldw + k0;
+  float* const turn = s_turn[warp];
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    if (n0 + j >= N) break;
+    float x[8];
+    word_values(w[j], step[j], a.one, x);
+    const bool whole = a.vec && k0 + 256 <= K;
+    if (sizeof(T) == 2 && whole) {  // 16 bytes a lane, in order
+      store8(out + j * a.ldw + 8 * lane, x);
+      continue;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) turn[9 * lane + e] = x[e];
+    __syncwarp();
+    if (whole) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const float* const t = turn + q * 144 + 4 * lane + lane / 2;
+        *reinterpret_cast<float4*>(out + j * a.ldw + q * 128 + 4 * lane) = make_float4(t[0], t[1], t[2], t[3]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (k0 + e * 32 + lane < K) out[j * a.ldw + e * 32 + lane] = from_f32<T>(turn[e * 36 + lane + lane / 8]);
+    }
   }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) k_w4_dequantize_cols(DequantArgs a) {
-  __shared__ float tile[32][kBlock + 1];
-  const int64_t kb = blockIdx.y, n0 = (int64_t)blockIdx.x * 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = lane & 15;
-  const int64_t k0 = kb * kBlock + 8 * i;
-  for (int r = 2 * warp + (lane >> 4); r < 32; r += 16) {
-    const int64_t n = n0 + r;
-    if (n < a.N && k0 < a.K) {
-      const uint32_t w = reinterpret_cast<const uint32_t*>(a.codes + n * a.ldc + kb * kBlockBytes)[word_of(i)];
-      const float step = a.steps[n * a.lds + k0 / a.group];
+__global__ void __launch_bounds__(512) k_w4_dequantize_cols(DequantArgs a) {
+  __shared__ uint32_t s_word[kColChannels][17];
+  __shared__ float s_step[4][kColChannels];
+  const int k0 = blockIdx.y * kBlock, n0 = blockIdx.x * kColChannels, K = (int)a.K, N = (int)a.N;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = k0 + 8 * warp, n = n0 + 2 * lane;
+  const int log8 = a.log_group - 3;  // a group is 2^log8 warps
 #pragma unroll
-      for (int e = 0; e < 8; ++e) tile[r][8 * i + e] = __fmul_rn(nibble_value(w, e), step);
-    }
+  for (int q = 0; q < kColChannels * 16 / 512; ++q) {
+    const int c = threadIdx.x / 16 + 32 * q;
+    s_word[c][threadIdx.x % 16] =
+        n0 + c < N ? reinterpret_cast<const uint32_t*>(a.codes + (n0 + c) * a.ldc + (int64_t)blockIdx.y * kBlockBytes)[threadIdx.x % 16] : 0u;
+  }
+  if (threadIdx.x < kColChannels << (4 - log8)) {
+    const int c = threadIdx.x % kColChannels, group = threadIdx.x / kColChannels, at = k0 + (group << a.log_group);
+    s_step[group][c] = n0 + c < N && at < K ? a.steps[(n0 + c) * a.lds + (at >> a.log_group)] : 0.f;
   }
   __syncthreads();
-  for (int r = warp; r < kBlock; r += 8) {
-    const int64_t k = kb * kBlock + r, n = n0 + lane;
-    if (k < a.K && n < a.N) static_cast<T*>(a.W)[k * a.ldw + n] = from_f32<T>(tile[lane][r]);
+  float x[2][8];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) word_values(s_word[2 * lane + j][word_of(warp)], s_step[warp >> log8][2 * lane + j], a.one, x[j]);
+  T* const out = static_cast<T*>(a.W) + k * a.ldw + n;
+  if (a.vec && k + 8 <= K && n + 1 < N) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (sizeof(T) == 4) *reinterpret_cast<float2*>(out + e * a.ldw) = make_float2(x[0][e], x[1][e]);
+      else *reinterpret_cast<uint32_t*>(out + e * a.ldw) = bf16_pair(x[0][e], x[1][e]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (k + e < K && n < N) out[e * a.ldw] = from_f32<T>(x[0][e]);
+      if (k + e < K && n + 1 < N) out[e * a.ldw + 1] = from_f32<T>(x[1][e]);
+    }
   }
 }
 
@@ -462,6 +559,14 @@ bool is_float(imq_dtype t) { return t == IMQ_F32 || t == IMQ_BF16; }
 int size_of(imq_dtype t) { return t == IMQ_F32 ? 4 : 2; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// Whether W may be read or written 16 bytes at a time along its rows (stored N x K), two entries (K x N).
+int vectors(const void* W, int64_t ldw, imq_dtype t, int32_t transW) {
+  const uintptr_t unit = transW ? 16 : 2 * size_of(t);
+  return ((reinterpret_cast<uintptr_t>(W) | (uintptr_t)(ldw * size_of(t))) & (unit - 1)) == 0;
+}
+
+int log2_of(int32_t group) { return group == 32 ? 5 : group == 64 ? 6 : 7; }
+
 int row_alignment(const void* p, int64_t row_bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(p) | (uintptr_t)row_bytes;
   return x % 16 == 0 ? 16 : x % 4 == 0 ? 4 : 2;
@@ -490,22 +595,22 @@ imq_status launch_w4_quantize(const void* W, imq_dtype wt, int64_t K, int64_t N,
   DeviceState* ds;
   s = device_state(&ds);
   if (s != IMQ_OK) return s;
-  QuantArgs a{W, K, N, ldw, codes, ldc, steps, lds, group, aligned16(W) && ldw * size_of(wt) % 16 == 0, ds->status};
-  const int64_t nb = (K + kBlock - 1) / kBlock;
+  QuantArgs a{W, K, N, ldw, codes, ldc, steps, lds, log2_of(group), vectors(W, ldw, wt, transW), ds->status};
   if (transW) {
-    const int64_t ctas = (N * nb + 15) / 16;
-    if (ctas > INT32_MAX) return IMQ_ERR_UNSUPPORTED;
+    const int64_t ctas = ((N + kRows - 1) / kRows * ((K + 255) / 256) + 7) / 8;
+    if (ctas > INT32_MAX / 8) return IMQ_ERR_UNSUPPORTED;
     if (wt == IMQ_F32)
       k_w4_quantize_rows<float><<<(unsigned)ctas, 256, 0, st>>>(a);
     else
       k_w4_quantize_rows<__nv_bfloat16><<<(unsigned)ctas, 256, 0, st>>>(a);
   } else {
+    const int64_t nb = (K + kBlock - 1) / kBlock;
     if (nb > 65535) return IMQ_ERR_UNSUPPORTED;
-    const dim3 grid((unsigned)((N + 31) / 32), (unsigned)nb);
+    const dim3 grid((unsigned)((N + kColChannels - 1) / kColChannels), (unsigned)nb);
     if (wt == IMQ_F32)
-      k_w4_quantize_cols<float><<<grid, 256, 0, st>>>(a);
+      k_w4_quantize_cols<float><<<grid, 512, 0, st>>>(a);
     else
-      k_w4_quantize_cols<__nv_bfloat16><<<grid, 256, 0, st>>>(a);
+      k_w4_quantize_cols<__nv_bfloat16><<<grid, 512, 0, st>>>(a);
   }
   return launched();
 }
@@ -517,22 +622,22 @@ imq_status launch_w4_dequantize(const uint8_t* codes, int64_t ldc, const float* 
   if (!is_float(wt) || (transW != 0 && transW != 1) || ldw < (transW ? K : N)) return IMQ_ERR_ARG;
   if (K == 0 || N == 0) return IMQ_OK;
   if (!W || (reinterpret_cast<uintptr_t>(W) & (size_of(wt) - 1))) return IMQ_ERR_ARG;
-  DequantArgs a{codes, ldc, steps, lds, K, N, group, W, ldw, aligned16(W) && ldw * size_of(wt) % 16 == 0};
-  const int64_t nb = (K + kBlock - 1) / kBlock;
+  DequantArgs a{codes, ldc, steps, lds, K, N, log2_of(group), W, ldw, vectors(W, ldw, wt, transW), kOneF16};
   if (transW) {
-    const int64_t ctas = (N * nb + 15) / 16;
-    if (ctas > INT32_MAX) return IMQ_ERR_UNSUPPORTED;
+    const int64_t ctas = ((N + kRows - 1) / kRows * ((K + 255) / 256) + 7) / 8;
+    if (ctas > INT32_MAX / 8) return IMQ_ERR_UNSUPPORTED;
     if (wt == IMQ_F32)
       k_w4_dequantize_rows<float><<<(unsigned)ctas, 256, 0, st>>>(a);
     else
       k_w4_dequantize_rows<__nv_bfloat16><<<(unsigned)ctas, 256, 0, st>>>(a);
   } else {
+    const int64_t nb = (K + kBlock - 1) / kBlock;
     if (nb > 65535) return IMQ_ERR_UNSUPPORTED;
-    const dim3 grid((unsigned)((N + 31) / 32), (unsigned)nb);
+    const dim3 grid((unsigned)((N + kColChannels - 1) / kColChannels), (unsigned)nb);
     if (wt == IMQ_F32)
-      k_w4_dequantize_cols<float><<<grid, 256, 0, st>>>(a);
+      k_w4_dequantize_cols<float><<<grid, 512, 0, st>>>(a);
     else
-      k_w4_dequantize_cols<__nv_bfloat16><<<grid, 256, 0, st>>>(a);
+      k_w4_dequantize_cols<__nv_bfloat16><<<grid, 512, 0, st>>>(a);
   }
   return launched();
 }

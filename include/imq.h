@@ -543,7 +543,7 @@ typedef struct {
  * slots   device int64[n], 8-byte aligned: the slot of each token; a negative one is skipped (padding).
  *         The slots of one call must differ; of two tokens on one slot it is not defined which one's
  *         codes and steps are kept.  A slot outside the cache is skipped and sets IMQ_ERR_BOUNDS in the
- *         status word.
+ *         status word.  IMQ_ERR_UNSUPPORTED for n * heads of 2^31 or more.
  */
 imq_status imq_kv_write(const imq_kv_cache *cache, const void *K, int64_t k_token_stride, int64_t k_head_stride,
                         const void *V, int64_t v_token_stride, int64_t v_head_stride, imq_dtype xt, int64_t n,
