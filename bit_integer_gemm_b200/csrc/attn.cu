@@ -8,9 +8,9 @@
 // query heads -- memory, far below the tensor cores' rate, but above what the fp32 units do at 8 query heads a
 // key head.  So both products run on warp-level tensor-core instructions, whose operands are registers: the
 // codes go from the copy to the operand without another trip through shared memory.
-//   - q * k runs on integers, exactly: a query row is scaled so that its largest entry becomes 2^23 - 2^15 - 2^7
-//     and rounded to an integer of three digits of radix 256 in -128 .. 127 (the unpacking of this library,
-//     applied to the query), and the stored bytes or nibbles are the other operand as they lie, offset and
+//   - q * k runs on integers, exactly: a query row is scaled so that its largest entry becomes nearly 2^23 and
+//     rounded to an integer of three digits of radix 256 in -128 .. 127 (the unpacking of this library, applied
+//     to the query), and the stored bytes or nibbles are the other operand as they lie, offset and
 //     all: the offset times the sum of a row's digits is what the sums start from.  8-bit codes need no
 //     conversion, 4-bit codes three instructions for eight.  Rows g and g + 8 of one 16-row operand hold the
 //     first two digits of up to 8 query heads, a second operand the third; for 9 to 16 heads each digit has
@@ -48,14 +48,16 @@ constexpr float kSlack = 3.f;          // how far, in powers of two, a weight ma
 constexpr float kStepSlack = 2.f;      // and how many times a step the unit of steps
 constexpr float kPScale = 2048.f;      // unit of the weights in fp16: 2^15 is the largest
 constexpr float kStepFloor = 1e-30f;   // the unit of the steps starts here
-constexpr float kQMax = 8355711.f;     // 127 * 65536 + 127 * 256 + 127
+constexpr float kQMax = 8355700.f;     // the largest query entry: below 127 * 65536 + 127 * 256 + 127 by more than its rounding
 
 struct AttnArgs {
   imq_kv_cache c;
   const void* Q;
   int64_t q_batch, q_head;
   int q_bf16, q_vec;  // q_vec: four entries of a row may be read at once
+  int o_bf16, o_vec;
   int group;          // query heads of a key head
+  int page_shift;     // page_size = 2^page_shift, or -1
   int head_chunks;    // blocks of up to 8 * kM query heads per key head
   const int32_t* table;
   int64_t table_stride;
@@ -66,7 +68,6 @@ struct AttnArgs {
   float scale;
   void* out;
   int64_t o_batch, o_head;
-  int o_bf16;
   float* lse;
   int64_t lse_batch;
   float* part;        // [CTA][2][head of the row][D]: sums of rows that several CTAs share
@@ -127,9 +128,23 @@ __device__ __forceinline__ void store_out(const AttnArgs& a, int64_t at, float v
   else
     static_cast<float*>(a.out)[at] = v;
 }
-// Four consecutive entries of out, aligned as they may be.
+// Four consecutive entries of out.
 __device__ __forceinline__ void store_out4(const AttnArgs& a, int64_t at, const float4& v) {
-  store_out(a, at, v.x), store_out(a, at + 1, v.y), store_out(a, at + 2, v.z), store_out(a, at + 3, v.w);
+  if (a.o_bf16) {
+    __nv_bfloat16* const p = static_cast<__nv_bfloat16*>(a.out) + at;
+    if (a.o_vec) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(v.x, v.y), bf16_pair(v.z, v.w));
+    } else {
+      p[0] = __float2bfloat16_rn(v.x), p[1] = __float2bfloat16_rn(v.y), p[2] = __float2bfloat16_rn(v.z), p[3] = __float2bfloat16_rn(v.w);
+    }
+  } else {
+    float* const p = static_cast<float*>(a.out) + at;
+    if (a.o_vec) {
+      *reinterpret_cast<float4*>(p) = v;
+    } else {
+      p[0] = v.x, p[1] = v.y, p[2] = v.z, p[3] = v.w;
+    }
+  }
 }
 
 // x as two fp16 parts (hi, lo), pairs packed.
@@ -145,6 +160,17 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 1 / x to the last bit or so: the hardware's approximation and a step of Newton's method.
+__device__ __forceinline__ float inverse(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return fmaf(y, fmaf(-x, y, 1.f), y);
 }
 __device__ __forceinline__ float minus_inf() { return __uint_as_float(0xFF800000u); }
 __device__ __forceinline__ float quiet_nan() { return __uint_as_float(0x7FC00000u); }
@@ -193,83 +219,87 @@ struct Shape {
   static constexpr int kSmem = kQBytes + (kWarps * kRing > kJoin ? kWarps * kRing : kJoin);
 };
 
-// The query operands of one row block: `load` reads four entries of a head.
-// Entry (step, operand, lane) is {row g at the step's first four inner positions of column c, row g + 8 at them,
+// The query operands of a row's heads.  A warp takes every fourth head, a lane its entries 4i .. 4i + 3 (and 128 further
+// on).  Entry (step, operand, lane) is {row g at the step's first four inner positions of column c, row g + 8 at them,
 // row g at the second four, row g + 8}; the positions are the ones whose codes a lane's words hold.
-template <int kBits, int kD, int kM, typename Load>
-__device__ __forceinline__ void prepare_query(uint4* qs, int32_t (*s_dig)[8 * kM], float* s_mul, int heads, float scale, int warp,
-                                              int lane, Load load) {
+template <int kBits, int kD, int kM>
+struct Query {
   using S = Shape<kBits, kD, kM>;
-  uint8_t* const bytes = reinterpret_cast<uint8_t*>(qs);
-  // a warp takes a head: lane i its entries 4i .. 4i + 3 (and 128 further on)
-  constexpr int kParts = (kD + 127) / 128;
-  for (int h = warp; h < heads; h += kWarps) {
-    float x[kParts][4] = {};
-    uint32_t key = 0;
+  static constexpr int kParts = (kD + 127) / 128, kMine = 8 * kM / kWarps;
+  float x[kMine][kParts][4];
+
+  template <typename T>
+  __device__ __forceinline__ void load(const T* q, int64_t head_stride, bool vec, int heads, int warp, int lane) {
 #pragma unroll
-    for (int p = 0; p < kParts; ++p)
-      if (4 * lane + 128 * p < kD) {
-        load(h, 4 * lane + 128 * p, x[p]);
+    for (int n = 0; n < kMine; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) key = max(key, abs_key(x[p][j]));
+      for (int p = 0; p < kParts; ++p) {
+        const int h = warp + n * kWarps, d = 4 * lane + 128 * p;
+        if (h < heads && d < kD) load4(q + h * head_stride + d, vec, x[n][p]);
+        else x[n][p][0] = x[n][p][1] = x[n][p][2] = x[n][p][3] = 0.f;
       }
-    key = __reduce_max_sync(0xffffffffu, key);
-    // r * max = kQMax but for a rounding; a row of (almost) zeros, and one that is not finite (its scores' factor is
-    // NaN), have digits of 0
-    const float top = __uint_as_float(key);
-    const bool use = key_finite(key) && top > 1e-30f;
-    const float r = use ? __fdiv_rn(kQMax, top) : 0.f;
-    if (lane == 0) s_mul[h] = !key_finite(key) ? quiet_nan() : use ? scale * kLog2e * __fdiv_rn(top, kQMax) : 0.f;
-    int32_t sum[3] = {};
+  }
+
+  __device__ __forceinline__ void write(uint8_t* qs, int32_t (*s_dig)[8 * kM], float* s_mul, int heads, float scale, int warp, int lane) {
 #pragma unroll
-    for (int p = 0; p < kParts; ++p) {
-      const int d = 4 * lane + 128 * p;
-      if (d >= kD) continue;
-      uint32_t dig[3] = {};  // this lane's four entries, a byte each
+    for (int n = 0; n < kMine; ++n) {
+      const int h = warp + n * kWarps;
+      if (h >= heads) break;
+      uint32_t key = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        int32_t v = use ? __float2int_rn(x[p][j] * r) : 0;
-        v = max(-8355711, min(8355711, v));
+      for (int p = 0; p < kParts; ++p)
 #pragma unroll
-        for (int k = 2; k >= 0; --k) {  // third, second, first digit
-          const int32_t low = (int32_t)(int8_t)(v & 255);
-          dig[k] |= (uint32_t)(low & 255) << (8 * j);
-          sum[k] += low;
-          v = (v - low) >> 8;
-        }
-      }
-      // where the four entries go: lane column, step and place of their codes
+        for (int j = 0; j < 4; ++j) key = max(key, abs_key(x[n][p][j]));
+      key = __reduce_max_sync(0xffffffffu, key);
+      // a row of (almost) zeros, and one that is not finite (its scores' factor is NaN), have digits of 0
+      const float top = __uint_as_float(key);
+      const bool use = key_finite(key) && top > 1e-30f;
+      const float r = use ? __fdividef(kQMax, fminf(top, 8e37f)) : 0.f;  // (the division is approximate below 2^126)
+      int32_t sum[3] = {};
 #pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        // kM = 1: operand 0 holds the first digit in row g and the second in row g + 8, operand 1 the third in row g;
-        // kM = 2: an operand a digit, heads g and g + 8
-        const int op = kM == 1 ? k / 2 : k, high = kM == 1 ? k % 2 : h / 8, g = kM == 1 ? h : h % 8;
+      for (int p = 0; p < kParts; ++p) {
+        const int d = 4 * lane + 128 * p;
+        if (kD % 128 != 0 && d >= kD) continue;
+        // v + 128 * (65536 + 256 + 1) has the digits, each plus 128, as its bytes
+        uint32_t u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[j] = (uint32_t)__float2int_rn(use ? fminf(fmaxf(x[n][p][j] * r, -kQMax), kQMax) : 0.f) + 0x808080u;
+        const uint32_t a = __byte_perm(u[0], u[1], 0x5140), b = __byte_perm(u[2], u[3], 0x5140);
+        const uint32_t e = __byte_perm(u[0], u[1], 0x0062), f = __byte_perm(u[2], u[3], 0x0062);
+        // first, second, third digits of the four entries
+        const uint32_t dig[3] = {__byte_perm(e, f, 0x5410) ^ 0x80808080u, __byte_perm(a, b, 0x7632) ^ 0x80808080u,
+                                 __byte_perm(a, b, 0x5410) ^ 0x80808080u};
         int c, w;
         S::KP::find(d, &c, &w);
-        if constexpr (kBits == 8) {
-          // four entries are one word of a key: inner step w / 2, its first or second four positions
-          reinterpret_cast<uint32_t*>(bytes)[((w / 2 * S::kQOps + op) * 32 + g * 4 + c) * 4 + (w % 2) * 2 + high] = dig[k];
-        } else {
-          // a word of a key is eight entries, its even nibbles (codes 0, 4, 1, 5) the first four positions of the
-          // step and its odd ones (codes 2, 6, 3, 7) the second; these four entries are codes 0-3 or 4-7
-          const int e = d % 8 / 4;
-          uint8_t* const to = bytes + (((w * S::kQOps + op) * 32 + g * 4 + c) * 4 + high) * 4;
-          to[e] = dig[k] & 255, to[e + 2] = dig[k] >> 8 & 255;            // codes 0 and 1 (4 and 5)
-          to[8 + e] = dig[k] >> 16 & 255, to[8 + e + 2] = dig[k] >> 24;   // codes 2 and 3 (6 and 7)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          sum[k] = __dp4a((int)dig[k], 0x01010101, sum[k]);
+          // kM = 1: operand 0 holds the first digit in row g and the second in row g + 8, operand 1 the third in row g;
+          // kM = 2: an operand a digit, heads g and g + 8
+          const int op = kM == 1 ? k / 2 : k, high = kM == 1 ? k % 2 : h / 8, g = kM == 1 ? h : h % 8;
+          if constexpr (kBits == 8) {
+            // four entries are one word of a key: inner step w / 2, its first or second four positions
+            reinterpret_cast<uint32_t*>(qs)[((w / 2 * S::kQOps + op) * 32 + g * 4 + c) * 4 + (w % 2) * 2 + high] = dig[k];
+          } else {
+            // a word of a key is eight entries, its even nibbles (codes 0, 4, 1, 5) the first four positions of the
+            // step and its odd ones (codes 2, 6, 3, 7) the second; these four entries are codes 0-3 or 4-7
+            uint8_t* const to = qs + (((w * S::kQOps + op) * 32 + g * 4 + c) * 4 + high) * 4 + d % 8 / 4;
+            to[0] = dig[k] & 255, to[2] = dig[k] >> 8 & 255;     // codes 0 and 1 (4 and 5)
+            to[8] = dig[k] >> 16 & 255, to[10] = dig[k] >> 24;   // codes 2 and 3 (6 and 7)
+          }
         }
       }
-    }
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      sum[k] = __reduce_add_sync(0xffffffffu, sum[k]);
-    }
-    // the offset of the stored codes times a row's digits: of the first two digits together, and of the third
-    if (lane == 0) {
-      s_dig[0][h] = -(1 << (kBits - 1)) * (256 * sum[0] + sum[1]);
-      s_dig[1][h] = -(1 << (kBits - 1)) * sum[2];
+      for (int k = 0; k < 3; ++k) sum[k] = __reduce_add_sync(0xffffffffu, sum[k]);
+      // the offset of the stored codes times a row's digits: of the first two digits together, and of the third
+      if (lane == 0) {
+        s_mul[h] = !key_finite(key) ? quiet_nan() : use ? scale * kLog2e * inverse(r) : 0.f;
+        s_dig[0][h] = -(1 << (kBits - 1)) * (256 * sum[0] + sum[1]);
+        s_dig[1][h] = -(1 << (kBits - 1)) * sum[2];
+      }
     }
   }
-}
+};
 
 template <int kBits, int kD, int kM>
 __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_attn(const __grid_constant__ AttnArgs a) {
@@ -282,18 +312,13 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
   __shared__ float s_mul[S::kHeads];
   __shared__ int32_t s_dig[2][S::kHeads];
   __shared__ float s_m[kWarps][S::kHeads], s_l[kWarps][S::kHeads];
+  __shared__ __align__(16) int s_part[8];  // the part of a row that the CTA works on
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-  const uint32_t rows = a.c.n_heads * a.head_chunks;
   asm volatile("griddepcontrol.launch_dependents;");
-  // rows of the operands that hold no head's digit stay zero (or as an earlier row of this CTA left them)
-  for (int i = threadIdx.x; i < S::kQBytes / 16; i += kWarps * 32) qs[i] = make_uint4(0u, 0u, 0u, 0u);
+  // the scores of rows without a head become 0 (their digits are whatever the shared memory holds)
   if (threadIdx.x < S::kHeads) s_mul[threadIdx.x] = 0.f, s_dig[0][threadIdx.x] = s_dig[1][threadIdx.x] = 0;
 
-  // ---- this CTA's part of the line: units u0 .. u1 - 1 (every warp finds it by itself)
-  uint32_t all = 0;
-  for (int i = lane; i < a.batch; i += 32) all += units_of(a, __ldg(a.lens + i));
-  all = __reduce_add_sync(0xffffffffu, all) * rows;
   // sequences without tokens, and those longer than the call covers, are answered here
   for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
     const int len = __ldg(a.lens + b);
@@ -306,56 +331,97 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
       for (int i = threadIdx.x; i < a.c.n_heads * a.group; i += kWarps * 32)
         a.lse[b * a.lse_batch + i] = over ? quiet_nan() : minus_inf();
   }
-  const uint32_t ctas = min((uint32_t)a.ctas, all);
-  if (blockIdx.x >= ctas) return;
-  const Parts parts(all, ctas);
-  uint32_t u0 = parts.begin(blockIdx.x);
-  const uint32_t u1 = parts.begin(blockIdx.x + 1);
-  // the sequence that u0 lies in, and the units before it
-  int b = 0;
-  uint32_t base = 0;
-  for (int i0 = 0;; i0 += 32) {
-    const uint32_t mine = i0 + lane < a.batch ? units_of(a, __ldg(a.lens + i0 + lane)) * rows : 0u;
-    uint32_t sum = mine;  // of the lanes up to this one
+
+  // ---- the first warp keeps the CTA's place in the line: units u0 .. u1 - 1, the sequence b that u0 lies in, and the
+  // units before it
+  uint32_t u0 = 0, u1 = 0, base = 0;
+  int b_now = 0;
+  const uint32_t rows = a.c.n_heads * a.head_chunks;
+  if (warp == 0) {
+    // inclusive sums of the first 32 sequences' units, and the sum of all
+    const uint32_t mine = lane < a.batch ? units_of(a, __ldg(a.lens + lane)) * rows : 0u;
+    uint32_t sum = mine;
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += x;
+      sum += lane >= o ? x : 0u;
     }
-    const unsigned behind = __ballot_sync(0xffffffffu, base + sum > u0);
-    if (behind || i0 + 32 >= a.batch) {
-      const int l = behind ? __ffs(behind) - 1 : 31;
-      b = i0 + l;
-      base += __shfl_sync(0xffffffffu, sum - mine, l);
-      break;
+    uint32_t all = __shfl_sync(0xffffffffu, sum, 31);
+    if (a.batch > 32) {
+      uint32_t more = 0;
+      for (int i = 32 + lane; i < a.batch; i += 32) more += units_of(a, __ldg(a.lens + i));
+      all += __reduce_add_sync(0xffffffffu, more) * rows;
     }
-    base += __shfl_sync(0xffffffffu, sum, 31);
+    const uint32_t ctas = min((uint32_t)a.ctas, all);
+    if (blockIdx.x < ctas) {
+      const Parts parts(all, ctas);
+      u0 = parts.begin(blockIdx.x), u1 = parts.begin(blockIdx.x + 1);
+      uint32_t own = mine;
+      for (;;) {
+        const unsigned behind = __ballot_sync(0xffffffffu, base + sum > u0);
+        if (behind) {
+          const int l = __ffs(behind) - 1;
+          b_now += l;
+          base += __shfl_sync(0xffffffffu, sum - own, l);
+          break;
+        }
+        base += __shfl_sync(0xffffffffu, sum, 31);
+        b_now += 32;
+        own = b_now + lane < a.batch ? units_of(a, __ldg(a.lens + b_now + lane)) * rows : 0u;
+        sum = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
+          sum += lane >= o ? x : 0u;
+        }
+      }
+    }
   }
 
-  __syncthreads();  // the operands are cleared
-
   // ---- a row's part after the other
-  while (u0 < u1) {
-    const int len = __ldg(a.lens + b);
-    const uint32_t per_row = units_of(a, len);
-    if (u0 - base >= per_row * rows) {
-      base += per_row * rows;
-      ++b;
-      continue;
+  for (;;) {
+    if (warp == 0) {
+      uint32_t take = 0, per_row = 0, row = 0, unit = 0;
+      int len = 0;
+      if (u0 < u1) {
+        for (;;) {
+          len = __ldg(a.lens + b_now);
+          per_row = units_of(a, len);
+          if (u0 - base < per_row * rows) break;
+          base += per_row * rows;
+          ++b_now;
+        }
+        row = (u0 - base) / per_row, unit = (u0 - base) - row * per_row, take = min(per_row - unit, u1 - u0);
+        u0 += take;
+      }
+      if (lane == 0) {
+        *reinterpret_cast<int4*>(s_part) = make_int4(b_now, (int)row, (int)unit, (int)take);
+        *reinterpret_cast<int2*>(s_part + 4) = make_int2(len, (int)per_row);
+      }
     }
-    const uint32_t row = (u0 - base) / per_row, unit = (u0 - base) % per_row, take = min(per_row - unit, u1 - u0);
-    u0 += take;
-    const int begin = (int)(unit * kUnit), end = min(len, begin + (int)(take * kUnit)), first = begin + warp * kTile;
-    const int kv = row / a.head_chunks, h0 = kv * a.group + row % a.head_chunks * S::kHeads;
-    const int heads = min(S::kHeads, (kv + 1) * a.group - h0);
+    __syncthreads();
+    const int4 part = *reinterpret_cast<const int4*>(s_part);
+    const int b = part.x, row = part.y, unit = part.z, take = part.w, len = s_part[4], per_row = s_part[5];
+    if (take == 0) return;
+    const int begin = unit * kUnit, end = min(len, begin + take * kUnit), first = begin + warp * kTile;
+    const int kv = a.head_chunks == 1 ? row : row / a.head_chunks;
+    const int h0 = kv * a.group + (row - kv * a.head_chunks) * S::kHeads, heads = min(S::kHeads, (kv + 1) * a.group - h0);
     const int32_t* const table = a.table + b * a.table_stride;
     const int n_tiles = first < end ? (end - first + kUnit - 1) / kUnit : 0;
+
+    Query<kBits, kD, kM> query;
+    {
+      const int64_t q0 = b * a.q_batch + h0 * a.q_head;
+      if (a.q_bf16) query.load(static_cast<const __nv_bfloat16*>(a.Q) + q0, a.q_head, a.q_vec, heads, warp, lane);
+      else query.load(static_cast<const float*>(a.Q) + q0, a.q_head, a.q_vec, heads, warp, lane);
+    }
 
     // Page and place (first token's position in it) of the warp's tiles i .. i + 31, one a lane.
     auto locate = [&](int i, int32_t& page, uint32_t& place) {
       i += lane;
       page = -1, place = 0;
       if (i < n_tiles) {
-        const uint32_t t = first + i * kUnit, j = t / (uint32_t)a.c.page_size;
+        const uint32_t t = first + i * kUnit, j = a.page_shift >= 0 ? t >> a.page_shift : t / (uint32_t)a.c.page_size;
         page = __ldg(table + j);
         place = t - j * (uint32_t)a.c.page_size;
         if (page >= a.c.n_pages) page = -1;
@@ -364,7 +430,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
     int32_t page_now, page_next;
     uint32_t place_now, place_next;
     locate(0, page_now, place_now);
-    locate(32, page_next, place_next);
+    page_next = -1, place_next = 0;
+    if (n_tiles > 32) locate(32, page_next, place_next);
 
     // ---- the warp's copies
     const uint32_t mine = smem_addr(ring) + warp * S::kRing;
@@ -431,18 +498,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
     for (int i = 0; i < kStages - 1; ++i) issue(i);
 
     // ---- the query operands, while the first copies are under way
-    const int64_t q0 = b * a.q_batch + h0 * a.q_head;
-    auto query = [&](const auto* Q, auto vec) {
-      prepare_query<kBits, kD, kM>(qs, s_dig, s_mul, heads, a.scale, warp, lane,
-                                   [&](int h, int d, float(&x)[4]) { load4(Q + q0 + h * a.q_head + d, vec, x); });
-    };
-    if (a.q_bf16) {
-      const auto* Q = static_cast<const __nv_bfloat16*>(a.Q);
-      if (a.q_vec) query(Q, std::true_type()); else query(Q, std::false_type());
-    } else {
-      const auto* Q = static_cast<const float*>(a.Q);
-      if (a.q_vec) query(Q, std::true_type()); else query(Q, std::false_type());
-    }
+    query.write(smem, s_dig, s_mul, heads, a.scale, warp, lane);
     __syncthreads();
     float mul[kM];
     int32_t start[2][kM];  // the offset's part of the first two digits' sums together, and of the third's
@@ -482,7 +538,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
             for (int j = 0; j < 2; ++j) {
               const uint32_t b0 = kBits == 8 ? w[j][kBits == 8 ? 2 * st : 0] : w[j][kBits == 8 ? 0 : st] & 0x0F0F0F0Fu;
               const uint32_t b1 = kBits == 8 ? w[j][kBits == 8 ? 2 * st + 1 : 0] : w[j][kBits == 8 ? 0 : st] >> 4 & 0x0F0F0F0Fu;
-              mma_s8u8(acc[j][op], q.x, q.y, q.z, q.w, b0, b1);
+              if (kM == 1 && op == 1) mma_s8u8(acc[j][op], q.x, 0u, q.z, 0u, b0, b1);  // rows 8-15 hold no digit
+              else mma_s8u8(acc[j][op], q.x, q.y, q.z, q.w, b0, b1);
             }
           }
         }
@@ -521,8 +578,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
         float vmax = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3])), fix[kM];
         vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
         vmax = fmaxf(fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2)), vref);
-        const float ratio = vref / vmax;
-        vref = vmax, winv = kPScale / vmax;
+        const float ratio = __fdividef(vref, vmax);
+        vref = vmax, winv = __fdividef(kPScale, vmax);
 #pragma unroll
         for (int r = 0; r < kM; ++r) {
           float top = fmaxf(fmaxf(p[r][0], p[r][1]), fmaxf(p[r][2], p[r][3]));
@@ -533,10 +590,12 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
           l[r] *= alpha;
           fix[r] = alpha * ratio;
         }
+        if (i > 0) {
 #pragma unroll
-        for (int n = 0; n < S::kCols; ++n) {
-          o[n][0] *= fix[0], o[n][1] *= fix[0];
-          o[n][2] *= fix[kM - 1], o[n][3] *= fix[kM - 1];
+          for (int n = 0; n < S::kCols; ++n) {
+            o[n][0] *= fix[0], o[n][1] *= fix[0];
+            o[n][2] *= fix[kM - 1], o[n][3] *= fix[kM - 1];
+          }
         }
       }
       uint32_t hi[kM][2], lo[kM][2];  // weights as operands
@@ -592,7 +651,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
     for (int r = 0; r < kM; ++r) {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      if (c == 0) s_m[warp][g + 8 * r] = m[r], s_l[warp][g + 8 * r] = bad ? quiet_nan() : l[r];
+      if (c == 0) s_m[warp][g + 8 * r] = m[r];
     }
     __syncthreads();  // the rings are done with: they hold the sums from here
     float* const sums = reinterpret_cast<float*>(ring);  // [warp][head][kPad]
@@ -601,7 +660,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
       float top = s_m[0][g + 8 * r];
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w][g + 8 * r]);
-      const float f = (top == minus_inf() ? 0.f : ex2(m[r] - top)) * (vref / kPScale);
+      const float weight = top == minus_inf() ? 1.f : ex2(m[r] - top), f = weight * (vref * (1.f / kPScale));
+      if (c == 0) s_l[warp][g + 8 * r] = bad ? quiet_nan() : l[r] * weight;
       float* const row = sums + (warp * S::kHeads + g + 8 * r) * S::kPad;
 #pragma unroll
       for (int n = 0; n < S::kCols; n += 8 / kBits * 2) {
@@ -622,29 +682,29 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
     __syncthreads();
     for (int i = threadIdx.x; i < heads * (kD / 4); i += kWarps * 32) {
       const int h = i / (kD / 4), d = i % (kD / 4) * 4;
-      float top = s_m[0][h];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w][h]);
-      const float ref = top == minus_inf() ? 0.f : top;
       float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
       float den = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float4 x = *reinterpret_cast<const float4*>(sums + (w * S::kHeads + h) * S::kPad + d);
         num.x += x.x, num.y += x.y, num.z += x.z, num.w += x.w;
-        den += ex2(s_m[w][h] - ref) * s_l[w][h];
+        den += s_l[w][h];
       }
-      if (take < per_row) {  // part of a row: the one that begins it in the second place
-        const int64_t at = (blockIdx.x * 2 + (unit == 0 ? 1 : 0)) * S::kHeads + h;
+      const bool shared = take < per_row;  // part of a row: the one that begins it in the second place
+      const int64_t at = (blockIdx.x * 2 + (unit == 0 ? 1 : 0)) * S::kHeads + h;
+      if (shared) {
         *reinterpret_cast<float4*>(a.part + at * kD + d) = num;
-        if (d == 0) a.ml[at] = make_float2(top, den);
       } else {
-        const float f = 1.f / den;
+        const float f = inverse(den);
         store_out4(a, b * a.o_batch + (h0 + h) * a.o_head + d, make_float4(num.x * f, num.y * f, num.z * f, num.w * f));
-        if (d == 0 && a.lse) a.lse[b * a.lse_batch + h0 + h] = kLn2 * (ref + log2f(den));
+      }
+      if (d == 0 && (shared || a.lse)) {
+        const float top = fmaxf(fmaxf(s_m[0][h], s_m[1][h]), fmaxf(s_m[2][h], s_m[3][h]));
+        if (shared) a.ml[at] = make_float2(top, den);
+        else a.lse[b * a.lse_batch + h0 + h] = kLn2 * ((top == minus_inf() ? 0.f : top) + lg2(den));
       }
     }
-    __syncthreads();  // before the next row's copies and operands
+    __syncthreads();  // before the next part's copies and operands
   }
 }
 
@@ -723,7 +783,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const __grid_cons
     }
   };
   auto write_lse = [&](int h, float ref, float sum) {
-    if (a.lse) a.lse[b * a.lse_batch + h0 + h] = kLn2 * ((ref == minus_inf() ? 0.f : ref) + log2f(sum));
+    if (a.lse) a.lse[b * a.lse_batch + h0 + h] = kLn2 * ((ref == minus_inf() ? 0.f : ref) + lg2(sum));
   };
   if (n <= kJoinWarps && !per_head) {
     for (int h = warp; h < heads; h += kJoinWarps) {
@@ -876,9 +936,12 @@ imq_status launch_paged_attention(const imq_kv_cache* c, const void* Q, imq_dtyp
   a.group = q_heads / c->n_heads;
   const int per = heads_of_cta(a.group);
   a.head_chunks = (a.group + per - 1) / per;
+  a.page_shift = (c->page_size & (c->page_size - 1)) == 0 ? __builtin_ctz(c->page_size) : -1;
   a.table = table, a.table_stride = table_stride, a.lens = lens, a.batch = (int)batch, a.limit = (int)max_len;
   a.scale = scale;
   a.out = out, a.o_batch = o_batch, a.o_head = o_head, a.o_bf16 = ot == IMQ_BF16;
+  const int64_t o_size = ot == IMQ_F32 ? 4 : 2;
+  a.o_vec = ((reinterpret_cast<uintptr_t>(out) | (uintptr_t)(o_batch * o_size) | (uintptr_t)(o_head * o_size)) & (4 * o_size - 1)) == 0;
   a.lse = lse, a.lse_batch = lse_batch;
   s = launch_main(a, {false, workspace, workspace_bytes, st});
   if (s != IMQ_OK || !has_parts(max_len)) return s;
