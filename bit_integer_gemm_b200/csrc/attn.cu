@@ -27,9 +27,9 @@
 // 2^11), so most tiles need no exchange between lanes.
 //
 // Split: the work of all sequences and key heads lies in one line of units of 64 tokens, cut into equal parts, one
-// for each CTA that the SMs hold at once; so lengths may differ as they will.  A CTA's four warps take tiles
-// of 16 tokens in turn, each with its own ring of asynchronous copies (every lane copies what it will use
-// itself, so a tile waits for no barrier but the warp's), and join in shared memory.  Rows that several CTAs
+// for each CTA that the SMs hold at once; so lengths may differ as they will.  A CTA's four warps take runs
+// of 16 tokens in turn, each with its own ring of asynchronous copies (so that a tile waits for no barrier but
+// the warp's), and join in shared memory.  Rows that several CTAs
 // share join in k_attn_join from partial sums in the workspace, in a fixed order.
 #include <atomic>
 #include <type_traits>
@@ -41,8 +41,8 @@ namespace imq {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kTile = 16;              // tokens of a warp's tile; it lies in one page (pages are multiples of it)
-constexpr int kUnit = kWarps * kTile;  // tokens: the grain of the split
+constexpr int kRun = 16;              // tokens that a warp copies at a time; they lie in one page (pages are multiples of it)
+constexpr int kUnit = kWarps * kRun;  // tokens: the grain of the split
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 3.f;          // how far, in powers of two, a weight may exceed the reference's,
 constexpr float kStepSlack = 2.f;      // and how many times a step the unit of steps
@@ -74,6 +74,7 @@ struct AttnArgs {
   float2* ml;         // [CTA][2][head of the row]: reference (a power of two's exponent) and sum of the weights
   int32_t* status;
   uint32_t one;       // kOneF16
+  uint32_t k_stride16, v_stride16, s_stride16;  // of pages, in 16 bytes
 };
 
 // Bytes a lane holds of a token's key (a quarter of the vector), as 16-byte pieces and an 8-byte one.  Piece p of the
@@ -206,11 +207,14 @@ struct Shape {
   static constexpr int kSteps = kD / 32;               // inner steps of q * k
   static constexpr int kCols = kD / 8;                 // 8-column blocks of p * v
   static constexpr int kValues = 16 * kRow, kStepsAt = kValues + 16 * kPitch;
-  static constexpr int kTileBytes = kStepsAt + 128;    // keys, values, steps of 16 tokens
-  // about 13 KB for a warp's ring: 16 warps an SM have 130 KB of copies under way
-  static constexpr int kStages = 13000 / kTileBytes < 2 ? 2 : 13000 / kTileBytes > 8 ? 8 : 13000 / kTileBytes;
+  static constexpr int kRunBytes = kStepsAt + 128;     // keys, values, steps of 16 tokens
+  // A tile is two runs where registers and shared memory allow: their chains of dependent instructions overlap.
+  static constexpr int kRuns = 1;
+  static constexpr int kTileBytes = kRuns * kRunBytes;
+  static constexpr int kBudget = 13000;  // of a warp's ring: three CTAs an SM have about 100 KB of copies under way
+  static constexpr int kStages = kBudget / kTileBytes < 2 ? 2 : kBudget / kTileBytes > 8 ? 8 : kBudget / kTileBytes;
   static constexpr int kRing = kStages * kTileBytes;
-  static constexpr int kPerSm = kD <= 128 ? 4 : 2;     // CTAs an SM, by the registers of the sums
+  static constexpr int kPerSm = kD <= 64 ? 4 : kD <= 128 ? 3 : 2;     // CTAs an SM, by the registers of the sums
   static constexpr int kHeads = 8 * kM;
   static constexpr int kQOps = kM + 1;                 // operands of the digits, 512 bytes each a step
   static constexpr int kQBytes = kSteps * kQOps * 512;
@@ -305,7 +309,7 @@ template <int kBits, int kD, int kM>
 __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_attn(const __grid_constant__ AttnArgs a) {
   using S = Shape<kBits, kD, kM>;
   using KP = typename S::KP;
-  constexpr int kStages = S::kStages, kRow = S::kRow;
+  constexpr int kStages = S::kStages, kRow = S::kRow, kRuns = S::kRuns;
   extern __shared__ __align__(16) uint8_t smem[];
   uint4* const qs = reinterpret_cast<uint4*>(smem);
   uint8_t* const ring = smem + S::kQBytes;
@@ -403,11 +407,11 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
     const int4 part = *reinterpret_cast<const int4*>(s_part);
     const int b = part.x, row = part.y, unit = part.z, take = part.w, len = s_part[4], per_row = s_part[5];
     if (take == 0) return;
-    const int begin = unit * kUnit, end = min(len, begin + take * kUnit), first = begin + warp * kTile;
+    const int begin = unit * kUnit, end = min(len, begin + take * kUnit), first = begin + warp * kRun;
     const int kv = a.head_chunks == 1 ? row : row / a.head_chunks;
     const int h0 = kv * a.group + (row - kv * a.head_chunks) * S::kHeads, heads = min(S::kHeads, (kv + 1) * a.group - h0);
     const int32_t* const table = a.table + b * a.table_stride;
-    const int n_tiles = first < end ? (end - first + kUnit - 1) / kUnit : 0;
+    const int n_runs = first < end ? (end - first + kUnit - 1) / kUnit : 0;
 
     Query<kBits, kD, kM> query;
     {
@@ -416,79 +420,82 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
       else query.load(static_cast<const float*>(a.Q) + q0, a.q_head, a.q_vec, heads, warp, lane);
     }
 
-    // Page and place (first token's position in it) of the warp's tiles i .. i + 31, one a lane.
-    auto locate = [&](int i, int32_t& page, uint32_t& place) {
-      i += lane;
-      page = -1, place = 0;
-      if (i < n_tiles) {
-        const uint32_t t = first + i * kUnit, j = a.page_shift >= 0 ? t >> a.page_shift : t / (uint32_t)a.c.page_size;
-        page = __ldg(table + j);
-        place = t - j * (uint32_t)a.c.page_size;
-        if (page >= a.c.n_pages) page = -1;
-      }
+    // Where the warp's runs u .. u + 31 lie, one a lane: the offsets of their page and place in the cache's keys, values
+    // and steps, in 16 bytes; kNowhere for a page outside the cache.
+    constexpr uint32_t kNowhere = 0xFFFFFFFFu;
+    struct Place {
+      uint32_t k, v, s;
     };
-    int32_t page_now, page_next;
-    uint32_t place_now, place_next;
-    locate(0, page_now, place_now);
-    page_next = -1, place_next = 0;
-    if (n_tiles > 32) locate(32, page_next, place_next);
+    auto locate = [&](int u) {
+      Place at{kNowhere, 0u, 0u};
+      u += lane;
+      if (u < n_runs) {
+        const uint32_t t = first + u * kUnit, j = a.page_shift >= 0 ? t >> a.page_shift : t / (uint32_t)a.c.page_size;
+        const int32_t page = __ldg(table + j);
+        const uint32_t place = t - j * (uint32_t)a.c.page_size + kv * (uint32_t)a.c.page_size;
+        if (page >= 0 && page < a.c.n_pages)
+          at = {page * a.k_stride16 + place * (kRow / 16), page * a.v_stride16 + place * (kRow / 16), page * a.s_stride16 + place / 2};
+      }
+      return at;
+    };
+    Place now = locate(0), next{kNowhere, 0u, 0u};
+    if (n_runs > 32) next = locate(32);
 
     // ---- the warp's copies
     const uint32_t mine = smem_addr(ring) + warp * S::kRing;
-    const uint8_t* const k_base = a.c.k + (int64_t)kv * a.c.page_size * kRow + g * kRow + c * 16;
-    const uint8_t* const v_base = a.c.v + (int64_t)kv * a.c.page_size * kRow + lane * 16;
-    const float* const s_base = a.c.steps + (int64_t)kv * a.c.page_size * 2 + lane * 4;
     bool bad = false;
-    uint32_t fill = mine;  // the stage that is filled next
+    uint32_t fill = mine;  // the tile that is filled next
     auto issue = [&](int i) {
-      if (i < n_tiles) {
-        if ((i & 31) == 0 && i > 0) {
-          page_now = page_next, place_now = place_next;
-          locate(i + 32, page_next, place_next);
-        }
-        const int32_t page = __shfl_sync(0xffffffffu, page_now, i & 31);
-        const uint32_t place = __shfl_sync(0xffffffffu, place_now, i & 31);
-        const int left = end - (first + i * kUnit);
-        const uint64_t p = (uint32_t)max(page, 0);
-        const uint8_t* kp = k_base + p * (uint32_t)a.c.k_page_stride + (uint64_t)place * (uint32_t)kRow;
-        const uint8_t* vp = v_base + p * (uint32_t)a.c.v_page_stride + (uint64_t)place * (uint32_t)kRow;
-        const float* sp = s_base + p * (uint32_t)a.c.steps_page_stride + (uint64_t)place * 2u;
-        const uint32_t to16 = fill + lane * 16, to8 = fill + lane * 8 + KP::n16 * 512;
-        if (left >= kTile && page >= 0) {
-          // keys: tokens g and g + 8, this lane's quarter; values: the tile's bytes in order
+      if (i * kRuns < n_runs) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-#pragma unroll
-            for (int q = 0; q < KP::n16; ++q) cp_async<16>(to16 + j * 8 * kRow + q * 512, kp + j * 8 * kRow + q * 64);
-            if (KP::n8) cp_async<8>(to8 + j * 8 * kRow, kp - 8 * c + j * 8 * kRow + 64 * KP::n16);
+        for (int r = 0; r < kRuns; ++r) {
+          const int u = i * kRuns + r, left = end - (first + u * kUnit);
+          if (r == 0 && (u & 31) == 0 && u > 0) {
+            now = next;
+            next = locate(u + 32);
           }
+          const uint32_t ko = __shfl_sync(0xffffffffu, now.k, u & 31), vo = __shfl_sync(0xffffffffu, now.v, u & 31);
+          const uint32_t so = __shfl_sync(0xffffffffu, now.s, u & 31);
+          const uint8_t* const kp = a.c.k + (uint64_t)ko * 16 + (g * kRow + c * 16);
+          const uint8_t* const vp = a.c.v + (uint64_t)vo * 16 + lane * 16;
+          const uint8_t* const sp = reinterpret_cast<const uint8_t*>(a.c.steps) + (uint64_t)so * 16 + lane * 16;
+          const uint32_t to = fill + r * S::kRunBytes, to16 = to + lane * 16, to8 = to + lane * 8 + KP::n16 * 512;
+          if (left >= kRun && ko != kNowhere) {
+            // keys: tokens g and g + 8, this lane's quarter; values: the run's bytes in order
 #pragma unroll
-          for (int q = 0; q < S::kChunks / 2; ++q) {
-            const int at = q * 32 + lane;
-            cp_async<16>(fill + S::kValues + S::chunk_at(at / S::kChunks, at % S::kChunks), vp + q * 512);
-          }
-          if (lane < 8) cp_async<16>(to16 + S::kStepsAt, sp);
-        } else {
-          // the end of the sequence, or a page outside the cache: what is not read is zero-filled (steps of 0: no
-          // stale value meets a weight of 0), with an address that is not read either
-          const int valid = page < 0 ? 0 : min(left, kTile);
-          bad |= page < 0;
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+              for (int q = 0; q < KP::n16; ++q) cp_async<16>(to16 + j * 8 * kRow + q * 512, kp + j * 8 * kRow + q * 64);
+              if (KP::n8) cp_async<8>(to8 + j * 8 * kRow, kp - 8 * c + j * 8 * kRow + 64 * KP::n16);
+            }
+#pragma unroll
+            for (int q = 0; q < S::kChunks / 2; ++q) {
+              const int at = q * 32 + lane;
+              cp_async<16>(to + S::kValues + S::chunk_at(at / S::kChunks, at % S::kChunks), vp + q * 512);
+            }
+            if (lane < 8) cp_async<16>(to16 + S::kStepsAt, sp);
+          } else {
+            // the end of the sequence, or a page outside the cache: what is not read is zero-filled (steps of 0: no
+            // stale value meets a weight of 0), with an address that is not read either
+            const int valid = ko == kNowhere ? 0 : min(max(left, 0), kRun);
+            bad |= ko == kNowhere && left > 0;
 #pragma unroll 1
-          for (int j = 0; j < 2; ++j) {
-            const bool on = 8 * j + g < valid;
-            const uint8_t* from = on ? kp + j * 8 * kRow : a.c.k;
+            for (int j = 0; j < 2; ++j) {
+              const bool on = 8 * j + g < valid;
+              const uint8_t* from = on ? kp + j * 8 * kRow : a.c.k;
 #pragma unroll
-            for (int q = 0; q < KP::n16; ++q) cp_async_part<16>(to16 + j * 8 * kRow + q * 512, from + (on ? q * 64 : 0), on ? 16u : 0u);
-            if (KP::n8) cp_async_part<8>(to8 + j * 8 * kRow, from + (on ? 64 * KP::n16 - 8 * c : 0), on ? 8u : 0u);
-          }
+              for (int q = 0; q < KP::n16; ++q) cp_async_part<16>(to16 + j * 8 * kRow + q * 512, from + (on ? q * 64 : 0), on ? 16u : 0u);
+              if (KP::n8) cp_async_part<8>(to8 + j * 8 * kRow, from + (on ? 64 * KP::n16 - 8 * c : 0), on ? 8u : 0u);
+            }
 #pragma unroll 1
-          for (int q = 0; q < S::kChunks / 2; ++q) {
-            const int at = q * 32 + lane;
-            const bool on = at / S::kChunks < valid;
-            cp_async_part<16>(fill + S::kValues + S::chunk_at(at / S::kChunks, at % S::kChunks), on ? vp + q * 512 : a.c.v, on ? 16u : 0u);
+            for (int q = 0; q < S::kChunks / 2; ++q) {
+              const int at = q * 32 + lane;
+              const bool on = at / S::kChunks < valid;
+              cp_async_part<16>(to + S::kValues + S::chunk_at(at / S::kChunks, at % S::kChunks), on ? vp + q * 512 : a.c.v, on ? 16u : 0u);
+            }
+            const int n = min(max(valid - 2 * lane, 0), 2);
+            if (lane < 8) cp_async_part<16>(to16 + S::kStepsAt, n ? sp : reinterpret_cast<const uint8_t*>(a.c.steps), 8u * n);
           }
-          const int n = min(max(valid - 2 * lane, 0), 2);
-          if (lane < 8) cp_async_part<16>(to16 + S::kStepsAt, n ? sp : a.c.steps, 8u * n);
         }
         fill = fill + S::kTileBytes == mine + S::kRing ? mine : fill + S::kTileBytes;
       }
@@ -509,6 +516,13 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
       for (int k = 0; k < 2; ++k) start[k][r] = s_dig[k][g + 8 * r];
     }
 
+    constexpr bool kQInRegs = kM == 1 && kD <= 128;  // at most 32 registers
+    uint4 qr[kQInRegs ? S::kSteps * S::kQOps : 1];
+    if constexpr (kQInRegs) {
+#pragma unroll
+      for (int i = 0; i < S::kSteps * S::kQOps; ++i) qr[i] = qs[i * 32 + lane];
+    }
+
     // ---- the warp's tiles
     float o[S::kCols][4] = {};
     float m[kM], l[kM], vref = kStepFloor, winv = kPScale / kStepFloor;
@@ -517,25 +531,26 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
     const uint8_t* tile = ring + warp * S::kRing;
 
 #pragma unroll 1
-    for (int i = 0; i < n_tiles; ++i) {
+    for (int i = 0; i * kRuns < n_runs; ++i) {
       cp_async_wait<kStages - 2>();
-      __syncwarp();  // the steps were copied by eight lanes; and every lane is done with the tile that is overwritten now
+      __syncwarp();  // other lanes copied parts of the tile; and every lane is done with the tile that is overwritten now
       issue(i + kStages - 1);
-      // ---- scores of two blocks of eight tokens; this lane's tokens are 2c, 2c + 1, 2c + 8, 2c + 9, its heads g
-      // (and g + 8)
-      float p[kM][4];
+      // ---- scores, two blocks of eight tokens a run; this lane's tokens of a run are 2c, 2c + 1, 2c + 8, 2c + 9, its
+      // heads g (and g + 8)
+      constexpr int kMine = 4 * kRuns;
+      float p[kM][kMine];
       {
-        int32_t acc[2][S::kQOps][4] = {};
-        uint32_t w[2][KP::kBytes / 4];
+        int32_t acc[2 * kRuns][S::kQOps][4] = {};
+        uint32_t w[2 * kRuns][KP::kBytes / 4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) read_pieces<KP>(tile + j * 8 * kRow, lane, w[j]);
+        for (int j = 0; j < 2 * kRuns; ++j) read_pieces<KP>(tile + (j >> 1) * S::kRunBytes + (j & 1) * 8 * kRow, lane, w[j]);
 #pragma unroll
         for (int st = 0; st < S::kSteps; ++st) {
 #pragma unroll
           for (int op = 0; op < S::kQOps; ++op) {
-            const uint4 q = qs[(st * S::kQOps + op) * 32 + lane];
+            const uint4 q = kQInRegs ? qr[kQInRegs ? st * S::kQOps + op : 0] : qs[(st * S::kQOps + op) * 32 + lane];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < 2 * kRuns; ++j) {
               const uint32_t b0 = kBits == 8 ? w[j][kBits == 8 ? 2 * st : 0] : w[j][kBits == 8 ? 0 : st] & 0x0F0F0F0Fu;
               const uint32_t b1 = kBits == 8 ? w[j][kBits == 8 ? 2 * st + 1 : 0] : w[j][kBits == 8 ? 0 : st] >> 4 & 0x0F0F0F0Fu;
               if (kM == 1 && op == 1) mma_s8u8(acc[j][op], q.x, 0u, q.z, 0u, b0, b1);  // rows 8-15 hold no digit
@@ -546,7 +561,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
 #pragma unroll
         for (int r = 0; r < kM; ++r)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < kMine; ++j) {
             const auto& x = acc[j >> 1];
             const int32_t d0 = kM == 1 ? x[0][j & 1] : x[0][2 * r + (j & 1)];
             const int32_t d1 = kM == 1 ? x[0][2 + (j & 1)] : x[kM - 1][2 * r + (j & 1)];
@@ -554,39 +569,50 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
             p[r][j] = fmaf((float)(d0 * 256 + d1 + start[0][r]), 256.f, (float)(d2 + start[1][r]));
           }
       }
-      const float4 st0 = *reinterpret_cast<const float4*>(tile + S::kStepsAt + c * 16);
-      const float4 st1 = *reinterpret_cast<const float4*>(tile + S::kStepsAt + 64 + c * 16);
-      const float ks[4] = {st0.x, st0.z, st1.x, st1.z}, vs[4] = {st0.y, st0.w, st1.y, st1.w};
-      const int left = end - (first + i * kUnit);
-      bool raise = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3])) > kStepSlack * vref;
+      float ks[kMine], vs[kMine];
+#pragma unroll
+      for (int j = 0; j < 2 * kRuns; ++j) {
+        const float4 st = *reinterpret_cast<const float4*>(tile + (j >> 1) * S::kRunBytes + S::kStepsAt + (j & 1) * 64 + c * 16);
+        ks[2 * j] = st.x, vs[2 * j] = st.y, ks[2 * j + 1] = st.z, vs[2 * j + 1] = st.w;
+      }
+      float vmax = vs[0];
+#pragma unroll
+      for (int j = 1; j < kMine; ++j) vmax = fmaxf(vmax, vs[j]);
+      bool raise = vmax > kStepSlack * vref;
 #pragma unroll
       for (int r = 0; r < kM; ++r)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) p[r][j] *= ks[j] * mul[r];
-      if (left < kTile) {
+        for (int j = 0; j < kMine; ++j) p[r][j] *= ks[j] * mul[r];
+      const int left = end - (first + i * kRuns * kUnit);  // run 1 of a tile lies kUnit tokens behind run 0
+      if (left < (kRuns - 1) * kUnit + kRun) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (8 * (j >> 1) + 2 * c + (j & 1) >= left) {
+        for (int j = 0; j < kMine; ++j)
+          if ((j >> 2) * kUnit + 8 * (j >> 1 & 1) + 2 * c + (j & 1) >= left) {
 #pragma unroll
             for (int r = 0; r < kM; ++r) p[r][j] = minus_inf();
           }
       }
+      float top[kM];
 #pragma unroll
-      for (int r = 0; r < kM; ++r) raise |= fmaxf(fmaxf(p[r][0], p[r][1]), fmaxf(p[r][2], p[r][3])) > m[r] + kSlack;
+      for (int r = 0; r < kM; ++r) {
+        top[r] = p[r][0];
+#pragma unroll
+        for (int j = 1; j < kMine; ++j) top[r] = fmaxf(top[r], p[r][j]);
+        raise |= top[r] > m[r] + kSlack;
+      }
       if (__any_sync(0xffffffffu, raise)) {
         // new references, the largest so far, and the sums in their units
-        float vmax = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3])), fix[kM];
+        float fix[kM];
         vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
         vmax = fmaxf(fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2)), vref);
         const float ratio = __fdividef(vref, vmax);
         vref = vmax, winv = __fdividef(kPScale, vmax);
 #pragma unroll
         for (int r = 0; r < kM; ++r) {
-          float top = fmaxf(fmaxf(p[r][0], p[r][1]), fmaxf(p[r][2], p[r][3]));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)), m[r]);
-          const float alpha = top == minus_inf() ? 1.f : ex2(m[r] - top);  // (no score yet but NaN)
-          m[r] = top;
+          top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+          top[r] = fmaxf(fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2)), m[r]);
+          const float alpha = top[r] == minus_inf() ? 1.f : ex2(m[r] - top[r]);  // (no score yet but NaN)
+          m[r] = top[r];
           l[r] *= alpha;
           fix[r] = alpha * ratio;
         }
@@ -598,45 +624,49 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
           }
         }
       }
-      uint32_t hi[kM][2], lo[kM][2];  // weights as operands
-      float vw[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) vw[j] = vs[j] * winv;
+      for (int j = 0; j < kMine; ++j) {
+        const float vw = vs[j] * winv;
 #pragma unroll
-      for (int r = 0; r < kM; ++r) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int r = 0; r < kM; ++r) {
           p[r][j] = ex2(p[r][j] - m[r]);
           l[r] += p[r][j];
-          p[r][j] *= vw[j];
+          p[r][j] *= vw;
         }
-        split_f16(p[r][0], p[r][1], &hi[r][0], &lo[r][0]);
-        split_f16(p[r][2], p[r][3], &hi[r][1], &lo[r][1]);
       }
-      auto product = [&](float (&acc)[4], uint32_t b0, uint32_t b1) {
-        if (kM == 1) {
-          mma_f16(acc, hi[0][0], lo[0][0], hi[0][1], lo[0][1], b0, b1);
-        } else {
-          mma_f16(acc, hi[0][0], hi[kM - 1][0], hi[0][1], hi[kM - 1][1], b0, b1);
-          mma_f16(acc, lo[0][0], lo[kM - 1][0], lo[0][1], lo[kM - 1][1], b0, b1);
+#pragma unroll
+      for (int run = 0; run < kRuns; ++run) {
+        uint32_t hi[kM][2], lo[kM][2];  // weights as operands
+#pragma unroll
+        for (int r = 0; r < kM; ++r) {
+          split_f16(p[r][4 * run], p[r][4 * run + 1], &hi[r][0], &lo[r][0]);
+          split_f16(p[r][4 * run + 2], p[r][4 * run + 3], &hi[r][1], &lo[r][1]);
         }
-      };
-#pragma unroll
-      for (int q = 0; q < S::kChunks; q += 2) {
-        // chunks q and q + 1 of tokens 0-7 and 8-15; a register holds two bytes (four nibbles) of tokens 2c and 2c + 1
-        uint32_t w[4];
-        ldmatrix_trans4(smem_addr(tile) + S::kValues + S::chunk_at(lane % 16, q + lane / 16), w);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t x = w[2 * e], y = w[2 * e + 1];
-          if constexpr (kBits == 8) {
-            product(o[2 * (q + e)], bytes_f16(x, 0x5250, a.one), bytes_f16(y, 0x5250, a.one));
-            product(o[2 * (q + e) + 1], bytes_f16(x, 0x5351, a.one), bytes_f16(y, 0x5351, a.one));
+        auto product = [&](float (&acc)[4], uint32_t b0, uint32_t b1) {
+          if (kM == 1) {
+            mma_f16(acc, hi[0][0], lo[0][0], hi[0][1], lo[0][1], b0, b1);
           } else {
-            product(o[4 * (q + e)], nibbles_f16<false>(x, a.one), nibbles_f16<false>(y, a.one));
-            product(o[4 * (q + e) + 1], nibbles_f16<true>(x, a.one), nibbles_f16<true>(y, a.one));
-            product(o[4 * (q + e) + 2], nibbles_f16<false>(x >> 8, a.one), nibbles_f16<false>(y >> 8, a.one));
-            product(o[4 * (q + e) + 3], nibbles_f16<true>(x >> 8, a.one), nibbles_f16<true>(y >> 8, a.one));
+            mma_f16(acc, hi[0][0], hi[kM - 1][0], hi[0][1], hi[kM - 1][1], b0, b1);
+            mma_f16(acc, lo[0][0], lo[kM - 1][0], lo[0][1], lo[kM - 1][1], b0, b1);
+          }
+        };
+#pragma unroll
+        for (int q = 0; q < S::kChunks; q += 2) {
+          // chunks q and q + 1 of tokens 0-7 and 8-15; a register holds two bytes (four nibbles) of tokens 2c and 2c + 1
+          uint32_t w[4];
+          ldmatrix_trans4(smem_addr(tile) + run * S::kRunBytes + S::kValues + S::chunk_at(lane % 16, q + lane / 16), w);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t x = w[2 * e], y = w[2 * e + 1];
+            if constexpr (kBits == 8) {
+              product(o[2 * (q + e)], bytes_f16(x, 0x5250, a.one), bytes_f16(y, 0x5250, a.one));
+              product(o[2 * (q + e) + 1], bytes_f16(x, 0x5351, a.one), bytes_f16(y, 0x5351, a.one));
+            } else {
+              product(o[4 * (q + e)], nibbles_f16<false>(x, a.one), nibbles_f16<false>(y, a.one));
+              product(o[4 * (q + e) + 1], nibbles_f16<true>(x, a.one), nibbles_f16<true>(y, a.one));
+              product(o[4 * (q + e) + 2], nibbles_f16<false>(x >> 8, a.one), nibbles_f16<false>(y >> 8, a.one));
+              product(o[4 * (q + e) + 3], nibbles_f16<true>(x >> 8, a.one), nibbles_f16<true>(y >> 8, a.one));
+            }
           }
         }
       }
@@ -712,7 +742,7 @@ constexpr int kJoinWarps = 8;
 
 // Joins the parts of a row that several CTAs hold.  Few parts: a warp takes a head; many: all warps share a head's
 // parts.  A lane has four entries (and four more at 128).  A CTA takes a row, or a head where the rows are few.
-__global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const __grid_constant__ AttnArgs a, int heads_of_cta, int per_head) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 4) k_attn_join(const __grid_constant__ AttnArgs a, int heads_of_cta, int per_head) {
   __shared__ float s_num[kJoinWarps][256], s_den[kJoinWarps], s_top[kJoinWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.y;
   const int D = a.c.head_dim;
@@ -739,13 +769,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const __grid_cons
 
   float top, den;
   float4 num[2];
-  // parts s, s + every, ...: eight at a time, so that their loads are under way together
+  // parts s, s + every, ...: four at a time, so that their loads are under way together
   auto add = [&](int h, int s, int every) {
     top = minus_inf(), den = 0.f;
     num[0] = num[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (; s < n; s += 8 * every) {
-      float2 ml[8];
-      float4 x[8];
+    for (; s < n; s += 4 * every) {
+      float2 ml[4];
+      float4 x[4];
       auto at = [&](int j) {
         const int t = min(s + j * every, n - 1);  // behind the last part: read, and not used
         return ((int64_t)(c0 + t) * 2 + (t == 0 ? 1 : 0)) * heads_of_cta + h;
@@ -753,20 +783,20 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const __grid_cons
       auto load = [&](int k) {
         if (4 * lane + 128 * k < D)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = *reinterpret_cast<const float4*>(a.part + at(j) * D + 4 * lane + 128 * k);
+          for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const float4*>(a.part + at(j) * D + 4 * lane + 128 * k);
       };
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ml[j] = a.ml[at(j)];
+      for (int j = 0; j < 4; ++j) ml[j] = a.ml[at(j)];
       load(0);
       float up = top;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) up = fmaxf(up, ml[j].x);
+      for (int j = 0; j < 4; ++j) up = fmaxf(up, ml[j].x);
       const float ref = up == minus_inf() ? 0.f : up, f = ex2(top - ref);
-      float w[8];
+      float w[4];
       top = up;
       den *= f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 4; ++j) {
         const bool on = s + j * every < n;
         w[j] = on ? ex2(ml[j].x - ref) : 0.f;
         den += on ? w[j] * ml[j].y : 0.f;
@@ -777,7 +807,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const __grid_cons
         if (k) load(k);
         num[k].x *= f, num[k].y *= f, num[k].z *= f, num[k].w *= f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 4; ++j)
           num[k].x += w[j] * x[j].x, num[k].y += w[j] * x[j].y, num[k].z += w[j] * x[j].z, num[k].w += w[j] * x[j].w;
       }
     }
@@ -930,6 +960,8 @@ imq_status launch_paged_attention(const imq_kv_cache* c, const void* Q, imq_dtyp
     return IMQ_ERR_ARG;
   AttnArgs a = {};
   a.c = *c;
+  a.k_stride16 = (uint32_t)(c->k_page_stride / 16), a.v_stride16 = (uint32_t)(c->v_page_stride / 16);
+  a.s_stride16 = (uint32_t)(c->steps_page_stride / 4);
   a.Q = Q, a.q_batch = q_batch, a.q_head = q_head, a.q_bf16 = qt == IMQ_BF16;
   const int64_t q_size = qt == IMQ_F32 ? 4 : 2;
   a.q_vec = ((qp | (uintptr_t)(q_batch * q_size) | (uintptr_t)(q_head * q_size)) & (4 * q_size - 1)) == 0;

@@ -232,11 +232,14 @@ imq_status check_cache(const imq_kv_cache* c) {
   if (c->bits != 4 && c->bits != 8) return IMQ_ERR_ARG;
   if (c->n_pages < 0 || c->n_heads < 1 || c->page_size < 1 || c->head_dim < 1) return IMQ_ERR_ARG;
   if (c->head_dim % 64 != 0 || c->head_dim > 256 || c->page_size % 16 != 0 || c->page_size > 65536 || c->n_heads > 65535 ||
-      c->n_pages > INT32_MAX || c->k_page_stride > UINT32_MAX || c->v_page_stride > UINT32_MAX || c->steps_page_stride > UINT32_MAX)
+      c->n_pages > INT32_MAX)
     return IMQ_ERR_UNSUPPORTED;
   const int64_t vectors = (int64_t)c->n_heads * c->page_size, bytes = vectors * (c->head_dim * c->bits / 8);
   if (c->k_page_stride < bytes || c->v_page_stride < bytes || c->steps_page_stride < 2 * vectors) return IMQ_ERR_ARG;
   if (c->k_page_stride % 16 || c->v_page_stride % 16 || c->steps_page_stride % 4) return IMQ_ERR_ARG;
+  // offsets into each of the three are 32-bit numbers of 16 bytes in places
+  const int64_t most = ((int64_t)1 << 36) - 16, pages = c->n_pages > 0 ? c->n_pages : 1;
+  if (c->k_page_stride > most / pages || c->v_page_stride > most / pages || c->steps_page_stride > most / 4 / pages) return IMQ_ERR_UNSUPPORTED;
   if (c->n_pages > 0 && (!c->k || !c->v || !c->steps)) return IMQ_ERR_ARG;
   if ((reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v) | reinterpret_cast<uintptr_t>(c->steps)) & 15)
     return IMQ_ERR_ARG;

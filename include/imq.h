@@ -525,8 +525,8 @@ imq_status imq_w4_matvec(const uint8_t *codes, int64_t ldc, const float *steps, 
  *           multiple of 16); within a page [n_heads][page_size][head_dim * bits / 8], contiguous.
  *   steps   fp32, 16-byte aligned: page p starts steps_page_stride floats after page p - 1 (a multiple of
  *           4); within a page [n_heads][page_size][2], the key's step and the value's.
- * bits 4 or 8.  head_dim 64, 128, 192 or 256; page_size a multiple of 16, at most 65536; at most 65535 heads; page
- * strides below 2^32 (else IMQ_ERR_UNSUPPORTED).
+ * bits 4 or 8.  head_dim 64, 128, 192 or 256; page_size a multiple of 16, at most 65536; at most 65535 heads; k, v and
+ * steps below 64 GiB each (else IMQ_ERR_UNSUPPORTED).
  */
 typedef struct {
   uint8_t *k, *v;
