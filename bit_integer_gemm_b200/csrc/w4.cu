@@ -292,23 +292,33 @@ constexpr int kMvWarps = 8;
 
 // kTiles: operands of 8 columns.  bf16: tokens 8t + g.  fp32: 1: part g % 3 of token g / 3; 3 (6): parts 0-2 of token g
 // (and of token g + 8).
-template <typename T, int kTiles, int kR>
+template <typename T, int kGroup, int kTiles, int kR>
 struct MvShape {
   static constexpr bool kF32 = sizeof(T) == 4;
   static constexpr bool kPacked = kF32 && kTiles == 1;
   static constexpr int kParts = kF32 ? 3 : 1;
   static constexpr int kTok = kPacked ? 1 : kTiles / kParts;  // tokens of a lane
   static constexpr int kXPieces = kTok * 4 * (kF32 ? 2 : 1);  // 16-byte pieces of X of a lane and block
-  static constexpr int kStage = (2 * kR + kXPieces) * 512 + 2 * kR * 128;
-  static constexpr int kStages = 12000 / kStage < 2 ? 2 : 12000 / kStage > 6 ? 6 : 12000 / kStage;
-  static constexpr int kCols = kTiles * 8 + 1;
+  static constexpr int kPerBlock = kBlock / kGroup;           // steps of a row and block
+  static constexpr int kStepsAt = (2 * kR + kXPieces) * 512;
+  static constexpr int kStage = kStepsAt + 2 * kR * 8 * kPerBlock * 4;
+  static constexpr int kPerSm = kTiles * kR <= 2 ? 2 : 1;     // CTAs an SM, by registers
+  static constexpr int kCols = kTiles * 8;
   static constexpr int kRed = kMvWarps * 16 * kR * kCols * 4;
+  // where a row's and column's sum of a warp lies: turned by a place every four rows, against bank conflicts
+  static __device__ __forceinline__ int sum_at(int warp, int row, int col) {
+    return ((warp * 16 * kR + row) * kTiles + col / 8) * 8 + ((col % 8 + row / 4) & 7);
+  }
+  // as many stages as shared memory holds (227 KB an SM, 1 KB a CTA of it reserved)
+  static constexpr int kFit = ((kPerSm == 2 ? 112 : 225) * 1024 - kRed) / (kMvWarps * kStage);
+  static constexpr int kStages = kFit > 6 ? 6 : kFit;
   static constexpr int kSmem = kMvWarps * kStages * kStage + kRed;
+  static_assert(kStages >= 2, "a ring needs two stages");
 };
 
 template <typename T, int kGroup, int kTiles, int kR>
-__global__ void __launch_bounds__(kMvWarps * 32, kTiles * kR <= 2 ? 2 : 1) k_w4_matvec(const __grid_constant__ MatvecArgs a) {
-  using S = MvShape<T, kTiles, kR>;
+__global__ void __launch_bounds__(kMvWarps * 32, MvShape<T, kGroup, kTiles, kR>::kPerSm) k_w4_matvec(const __grid_constant__ MatvecArgs a) {
+  using S = MvShape<T, kGroup, kTiles, kR>;
   constexpr int kStages = S::kStages, kPer16 = 16 / sizeof(T);
   extern __shared__ __align__(16) uint8_t smem[];
   float* const red = reinterpret_cast<float*>(smem + kMvWarps * kStages * S::kStage);
@@ -319,7 +329,7 @@ __global__ void __launch_bounds__(kMvWarps * 32, kTiles * kR <= 2 ? 2 : 1) k_w4_
   const int sets = (N + 16 * kR - 1) / (16 * kR);
   const int per_set = (nb - warp + kMvWarps - 1) / kMvWarps;  // this warp's blocks of a set (0 for K below its first)
   const int groups = (K + kGroup - 1) / kGroup;
-  constexpr int kPerBlock = kBlock / kGroup;
+  constexpr int kPerBlock = S::kPerBlock;
   uint8_t* const mine = smem + warp * kStages * S::kStage;
 
   // Columns without a token hold what lies in shared memory: a column's sums depend on no other column, and theirs are
@@ -350,12 +360,12 @@ __global__ void __launch_bounds__(kMvWarps * 32, kTiles * kR <= 2 ? 2 : 1) k_w4_
   auto issue = [&]() {
     if (set_in < sets && per_set > 0) {
       uint8_t* const to = mine + stage_in * S::kStage;
-      const uint32_t dst = smem_addr(to) + lane * 16, dst4 = smem_addr(to) + (2 * kR + S::kXPieces) * 512 + lane * 4;
+      const uint32_t dst = smem_addr(to) + lane * 16, dst4 = smem_addr(to) + S::kStepsAt + (g * kPerBlock + c) * 4;
       const bool steps_on = c < kPerBlock && kb_in * kPerBlock + c < groups;
 #pragma unroll
       for (int r = 0; r < 2 * kR; ++r) {
         cp_async<16>(dst + r * 512, code_row[r] + kb_in * kBlockBytes);
-        if (steps_on) cp_async<4>(dst4 + r * 128, step_row[r] + kb_in * kPerBlock);
+        if (steps_on) cp_async<4>(dst4 + r * 32 * kPerBlock, step_row[r] + kb_in * kPerBlock);
       }
       const int k0 = kb_in * kBlock;
       constexpr int kPieces = 8 / kPer16;  // of eight entries
@@ -369,7 +379,17 @@ __global__ void __launch_bounds__(kMvWarps * 32, kTiles * kR <= 2 ? 2 : 1) k_w4_
               for (int q = 0; q < kPieces; ++q)
                 cp_async<16>(dst + (2 * kR + (t * 4 + h) * kPieces + q) * 512, xp[t] + k0 + 32 * h + q * kPer16);
           }
-      } else {  // the end of a row, or rows that begin anywhere: four bytes at a time, or an entry
+      } else if (a.aligned >= 4 && k0 + kBlock <= K) {  // rows that begin anywhere: four bytes at a time
+#pragma unroll
+        for (int t = 0; t < S::kTok; ++t)
+          if (has[t]) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+#pragma unroll
+              for (int e = 0; e < 2 * (int)sizeof(T); ++e)
+                cp_async<4>(dst + (2 * kR + (t * 4 + h) * kPieces + e / 4) * 512 + e % 4 * 4, xp[t] + k0 + 32 * h + e * (4 / (int)sizeof(T)));
+          }
+      } else {  // the end of a row: four bytes at a time, or an entry
 #pragma unroll 1
         for (int h = 0; h < 4 * S::kTok; ++h) {
           const int t = h / 4, k = k0 + 32 * (h % 4);
@@ -416,7 +436,7 @@ __global__ void __launch_bounds__(kMvWarps * 32, kTiles * kR <= 2 ? 2 : 1) k_w4_
       for (int r = 0; r < kR; ++r)
 #pragma unroll
         for (int j = 0; j < 2; ++j) v[r][j] = *reinterpret_cast<const uint4*>(from + (2 * r + j) * 512 + lane * 16);
-      const float* const st = reinterpret_cast<const float*>(from + (2 * kR + S::kXPieces) * 512);
+      const float* const st = reinterpret_cast<const float*>(from + S::kStepsAt) + g * kPerBlock;
       float acc[kR][kTiles][4];
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
@@ -470,7 +490,7 @@ __global__ void __launch_bounds__(kMvWarps * 32, kTiles * kR <= 2 ? 2 : 1) k_w4_
           }
           if (closes) {
             const int gi = h * 32 / kGroup;
-            const float d0 = st[(2 * r) * 32 + g * 4 + gi], d1 = st[(2 * r + 1) * 32 + g * 4 + gi];
+            const float d0 = st[2 * r * 8 * kPerBlock + gi], d1 = st[(2 * r + 1) * 8 * kPerBlock + gi];
 #pragma unroll
             for (int t = 0; t < kTiles; ++t) {
               total[r][t][0] += d0 * acc[r][t][0], total[r][t][1] += d0 * acc[r][t][1];
@@ -485,9 +505,8 @@ __global__ void __launch_bounds__(kMvWarps * 32, kTiles * kR <= 2 ? 2 : 1) k_w4_
     for (int r = 0; r < kR; ++r)
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
-        float* const at = red + (warp * 16 * kR + 16 * r + g) * S::kCols + 8 * t + 2 * c;
-        at[0] = total[r][t][0], at[1] = total[r][t][1];
-        at[8 * S::kCols] = total[r][t][2], at[8 * S::kCols + 1] = total[r][t][3];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) red[S::sum_at(warp, 16 * r + g + 8 * (j >> 1), 8 * t + 2 * c + (j & 1))] = total[r][t][j];
       }
     __syncthreads();
     for (int o = threadIdx.x; o < 16 * kR * tokens; o += kMvWarps * 32) {
@@ -497,7 +516,7 @@ __global__ void __launch_bounds__(kMvWarps * 32, kTiles * kR <= 2 ? 2 : 1) k_w4_
       for (int p = S::kParts - 1; p >= 0; --p) {  // the smallest parts first
         const int col = S::kPacked ? 3 * tok + p : S::kF32 ? (tok / 8 * 3 + p) * 8 + tok % 8 : tok;
 #pragma unroll
-        for (int w = 0; w < kMvWarps; ++w) y += red[(w * 16 * kR + row) * S::kCols + col];
+        for (int w = 0; w < kMvWarps; ++w) y += red[S::sum_at(w, row, col)];
       }
       if (n < N) {
         const int64_t at = (m0 + tok) * a.ldy + n;
@@ -514,7 +533,7 @@ __global__ void __launch_bounds__(kMvWarps * 32, kTiles * kR <= 2 ? 2 : 1) k_w4_
 
 template <typename T, int kGroup, int kTiles, int kR>
 imq_status matvec_shape(const MatvecArgs& a, int num_sms, cudaStream_t st) {
-  constexpr int kSmem = MvShape<T, kTiles, kR>::kSmem;
+  constexpr int kSmem = MvShape<T, kGroup, kTiles, kR>::kSmem;
   const void* fn = reinterpret_cast<const void*>(&k_w4_matvec<T, kGroup, kTiles, kR>);
   static std::atomic<int> resident[64];  // CTAs an SM holds, per device; 0: not asked yet
   int dev = 0;
