@@ -596,6 +596,15 @@ def _empty(like: torch.Tensor, shape, dtype, stream):
         return like.new_empty(shape, dtype=dtype)
 
 
+def _matrix(t: torch.Tensor, what: str):
+    """(rows, columns, row stride) of a matrix with unit column stride."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{what} must be a matrix with unit column stride")
+    rows, cols = shape
+    return rows, cols, stride[0] if rows > 1 else cols
+
+
 class W4Weight:
     """A weight in 4 bits (K inputs, N output channels, a step per `group` inputs): `codes` (N, bytes of a row)
     uint8 and `steps` (N, groups) float32 in the storage of include/imq.h, both with unit column stride."""
@@ -604,15 +613,16 @@ class W4Weight:
         K, N, group = int(K), int(N), int(group)
         if group not in (32, 64, 128):
             raise ValueError(f"group must be 32, 64 or 128, not {group}")
-        if codes.dtype != torch.uint8 or codes.dim() != 2 or steps.dtype != torch.float32 or steps.dim() != 2:
+        if codes.dtype != torch.uint8 or steps.dtype != torch.float32:
             raise ValueError("codes must be a uint8 and steps a float32 matrix")
-        if codes.size(0) != N or steps.size(0) != N or codes.size(1) < self.row_bytes(K) or steps.size(1) < -(-K // group):
+        nc, row, ldc = _matrix(codes, "codes")
+        ns, groups, lds = _matrix(steps, "steps")
+        if nc != N or ns != N or row < self.row_bytes(K) or groups < -(-K // group):
             raise ValueError(f"codes {tuple(codes.shape)} and steps {tuple(steps.shape)} do not hold {K} x {N} in groups of {group}")
         if codes.device != steps.device:
             raise ValueError("codes and steps must be on one device")
         self.codes, self.steps, self.K, self.N, self.group = codes, steps, K, N, group
-        ldc, lds = (_ld(t) if t.numel() else t.size(1) for t in (codes, steps))
-        self._args = (codes.data_ptr(), ldc, steps.data_ptr(), lds, K, N, group)
+        self._args = (codes.data_ptr(), ldc if row else 0, steps.data_ptr(), lds if groups else 0, K, N, group)
 
     @staticmethod
     def row_bytes(K: int) -> int:
@@ -623,16 +633,19 @@ def imq_w4_quantize(W: torch.Tensor, group: int = 128, transW: bool = False, cod
                     stream=None) -> W4Weight:
     """A float32 or bfloat16 weight, stored K x N (N x K when transW), in 4 bits."""
     wt = _float_dtype(W.dtype, "W")
+    rows, cols, ld = _matrix(W, "W")
+    K, N = (cols, rows) if transW else (rows, cols)
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, not {group}")
     dev = _device(W, codes, steps)
-    ld = _ld(W)
-    N, K = W.shape if transW else (W.shape[1], W.shape[0])
     if codes is None:
         codes = _empty(W, (N, W4Weight.row_bytes(K)), torch.uint8, stream)
     if steps is None:
-        steps = _empty(W, (N, -(-K // int(group)) if int(group) > 0 else 0), torch.float32, stream)
+        steps = _empty(W, (N, -(-K // group)), torch.float32, stream)
     w = W4Weight(codes, steps, K, N, group)
-    _check(lib().imq_w4_quantize(W.data_ptr(), wt, K, N, ld, int(transW), w.group, *w._args[:4],
-                                 _raw_stream(stream, dev)), "imq_w4_quantize")
+    st = lib().imq_w4_quantize(W.data_ptr(), wt, K, N, ld, int(transW), group, *w._args[:4], _raw_stream(stream, dev))
+    if st:
+        _check(st, "imq_w4_quantize")
     return w
 
 
@@ -640,32 +653,43 @@ def imq_w4_dequantize(weight: W4Weight, dtype=torch.float32, transW: bool = Fals
     """The values of a 4-bit weight, K x N (N x K when transW)."""
     shape = (weight.N, weight.K) if transW else (weight.K, weight.N)
     if out is None:
-        out = _empty(weight.codes, shape, dtype, stream)
-    elif tuple(out.shape) != shape:
-        raise ValueError(f"out must be {shape}")
-    wt = _float_dtype(out.dtype, "out")
+        wt, ld = _float_dtype(dtype, "out"), shape[1]
+        out = _empty(weight.steps, shape, dtype, stream)
+    else:
+        wt = _float_dtype(out.dtype, "out")
+        rows, cols, ld = _matrix(out, "out")
+        if (rows, cols) != shape:
+            raise ValueError(f"out must be {shape}")
     dev = _device(weight.codes, out)
-    _check(lib().imq_w4_dequantize(*weight._args, out.data_ptr(), wt, _ld(out), int(transW), _raw_stream(stream, dev)),
-           "imq_w4_dequantize")
+    st = lib().imq_w4_dequantize(*weight._args, out.data_ptr(), wt, ld, int(transW), _raw_stream(stream, dev))
+    if st:
+        _check(st, "imq_w4_dequantize")
     return out
 
 
 def imq_w4_matvec(weight: W4Weight, X: torch.Tensor, out=None, out_dtype=None, stream=None) -> torch.Tensor:
     """X (M x K) times a 4-bit weight: M x N in out's dtype, out_dtype, or X's."""
-    xt = _float_dtype(X.dtype, "X")
-    if X.dim() != 2 or X.size(1) != weight.K or (X.stride(1) != 1 and weight.K > 1):
-        raise ValueError(f"X must be M x {weight.K} with unit column stride, not {tuple(X.shape)}")
-    M, N = X.size(0), weight.N
+    dtype = X.dtype
+    xt = _float_dtype(dtype, "X")
+    M, K, ldx = _matrix(X, "X")
+    N = weight.N
+    if K != weight.K:
+        raise ValueError(f"X must be M x {weight.K}, not {M} x {K}")
     if out is None:
-        yt = xt if out_dtype is None else _float_dtype(out_dtype, "out")
-        out, ldy = _empty(X, (M, N), X.dtype if out_dtype is None else out_dtype, stream), N
+        if out_dtype is None or out_dtype is dtype:
+            yt = xt
+            out = _empty(X, (M, N), dtype, stream)
+        else:
+            yt = _float_dtype(out_dtype, "out")
+            out = _empty(X, (M, N), out_dtype, stream)
+        ldy = N
     else:
-        yt, ldy = _float_dtype(out.dtype, "out"), _ld(out)
-        if tuple(out.shape) != (M, N) or (out_dtype is not None and out.dtype != out_dtype):
+        yt = _float_dtype(out.dtype, "out")
+        rows, cols, ldy = _matrix(out, "out")
+        if rows != M or cols != N or (out_dtype is not None and out.dtype != out_dtype):
             raise ValueError(f"out must be {M} x {N} of the output's dtype")
     dev = _device(weight.codes, X, out)
-    st = lib().imq_w4_matvec(*weight._args, X.data_ptr(), xt, M, X.stride(0) if M > 1 else weight.K, out.data_ptr(), yt, ldy,
-                             _raw_stream(stream, dev))
+    st = lib().imq_w4_matvec(*weight._args, X.data_ptr(), xt, M, ldx, out.data_ptr(), yt, ldy, _raw_stream(stream, dev))
     if st:
         _check(st, "imq_w4_matvec")
     return out
@@ -707,28 +731,32 @@ class KVCache:
         return cls(k, torch.zeros_like(k), torch.zeros((n_pages, n_heads, page_size, 2), device=device), head_dim, bits)
 
 
-def _vectors(t, cache: KVCache, n: int, what: str):
-    """(pointer, token stride, head stride) of (n, heads, head_dim) vectors."""
-    if t.shape != (n, cache.n_heads, cache.head_dim) or t.stride(2) != 1:
-        raise ValueError(f"{what} must be ({n}, {cache.n_heads}, {cache.head_dim}) with unit stride in the last axis")
-    return t.data_ptr(), t.stride(0), t.stride(1)
+def _vector_strides(t, shape, what: str):
+    """(token stride, head stride) of (n, heads, head_dim) vectors."""
+    stride = t.stride()
+    if t.shape != shape or stride[2] != 1:
+        raise ValueError(f"{what} must be {shape} with unit stride in the last axis")
+    return stride[0], stride[1]
 
 
 def _slots(slots) -> int:
-    if slots.dtype != torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
+    if slots.dtype is not torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
         raise ValueError("slots must be a contiguous int64 vector")
     return slots.size(0)
 
 
 def imq_kv_write(cache: KVCache, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, stream=None):
     """Quantises the tokens' keys and values (n, heads, head_dim) into their slots; negative slots are skipped."""
-    xt = _float_dtype(K.dtype, "K")
-    if V.dtype != K.dtype:
+    dtype = K.dtype
+    xt = _float_dtype(dtype, "K")
+    if V.dtype is not dtype:
         raise ValueError("K and V must have one dtype")
     n = _slots(slots)
+    shape = (n, cache.n_heads, cache.head_dim)
+    kt, kh = _vector_strides(K, shape, "K")
+    vt, vh = _vector_strides(V, shape, "V")
     dev = _device(cache.k, K, V, slots)
-    st = lib().imq_kv_write(cache._ref, *_vectors(K, cache, n, "K"), *_vectors(V, cache, n, "V"), xt, n, slots.data_ptr(),
-                            _raw_stream(stream, dev))
+    st = lib().imq_kv_write(cache._ref, K.data_ptr(), kt, kh, V.data_ptr(), vt, vh, xt, n, slots.data_ptr(), _raw_stream(stream, dev))
     if st:
         _check(st, "imq_kv_write")
 
@@ -737,17 +765,25 @@ def imq_kv_read(cache: KVCache, slots: torch.Tensor, dtype=torch.float32, K=None
     """(K, V) of the slots, each (n, heads, head_dim).  Rows of negative slots are left as they were: not
     initialised where this call allocates the output."""
     n = _slots(slots)
-    shape = (n, cache.n_heads, cache.head_dim)
+    heads, dim = cache.n_heads, cache.head_dim
+    shape = (n, heads, dim)
+    if K is not None or V is not None:
+        dtype = (V if K is None else K).dtype
+    yt = _float_dtype(dtype, "K and V")
     if K is None:
-        K = _empty(cache.steps, shape, dtype if V is None else V.dtype, stream)
+        kt, kh = heads * dim, dim
+        K = _empty(cache.steps, shape, dtype, stream)
+    else:
+        kt, kh = _vector_strides(K, shape, "K")
     if V is None:
-        V = _empty(K, shape, K.dtype, stream)
-    yt = _float_dtype(K.dtype, "K")
-    if V.dtype != K.dtype:
-        raise ValueError("K and V must have one dtype")
+        vt, vh = heads * dim, dim
+        V = _empty(cache.steps, shape, dtype, stream)
+    else:
+        vt, vh = _vector_strides(V, shape, "V")
+        if V.dtype is not dtype:
+            raise ValueError("K and V must have one dtype")
     dev = _device(cache.k, slots, K, V)
-    st = lib().imq_kv_read(cache._ref, slots.data_ptr(), n, *_vectors(K, cache, n, "K"), *_vectors(V, cache, n, "V"), yt,
-                           _raw_stream(stream, dev))
+    st = lib().imq_kv_read(cache._ref, slots.data_ptr(), n, K.data_ptr(), kt, kh, V.data_ptr(), vt, vh, yt, _raw_stream(stream, dev))
     if st:
         _check(st, "imq_kv_read")
     return K, V
@@ -771,45 +807,57 @@ def imq_paged_attention(cache: KVCache, Q: torch.Tensor, block_table: torch.Tens
     """Attention of one token per sequence, Q (batch, query heads, head_dim), over the sequences' cached tokens:
     (out, lse), lse None unless wanted.  block_table int32 (batch, pages of the longest), seq_lens int32 (batch).
     max_len bounds seq_lens (default: what the table covers); scale defaults to head_dim ** -0.5."""
-    qt = _float_dtype(Q.dtype, "Q")
-    D = cache.head_dim
-    if Q.dim() != 3 or Q.size(2) != D or Q.stride(2) != 1:
+    dtype, D = Q.dtype, cache.head_dim
+    qt = _float_dtype(dtype, "Q")
+    shape, stride = Q.shape, Q.stride()
+    if len(shape) != 3 or shape[2] != D or stride[2] != 1:
         raise ValueError(f"Q must be (batch, query heads, {D}) with unit stride in the last axis")
-    batch, heads, _ = shape = Q.shape
+    batch, heads, _ = shape
     if heads == 0 or heads % cache.n_heads:
         raise ValueError(f"{heads} query heads on {cache.n_heads} key heads")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.size(0) != batch or (
-            block_table.size(1) > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be int32 (batch, pages) with unit stride in the last axis")
-    if seq_lens.dtype != torch.int32 or seq_lens.shape != (batch,) or not seq_lens.is_contiguous():
+    if block_table.dtype is not torch.int32:
+        raise ValueError("block_table must be int32")
+    rows, width, table_stride = _matrix(block_table, "block_table")
+    if rows != batch:
+        raise ValueError(f"block_table must have a row for each of {batch} sequences")
+    if seq_lens.dtype is not torch.int32 or seq_lens.shape != (batch,) or not seq_lens.is_contiguous():
         raise ValueError("seq_lens must be a contiguous int32 vector of the batch")
-    width = block_table.size(1)
     max_len = width * cache.page_size if max_len is None else int(max_len)
     if out is None:
-        ot = qt if out_dtype is None else _float_dtype(out_dtype, "out")
-        out = _empty(Q, shape, Q.dtype if out_dtype is None else out_dtype, stream)
+        if out_dtype is None or out_dtype is dtype:
+            ot = qt
+            out = _empty(Q, shape, dtype, stream)
+        else:
+            ot = _float_dtype(out_dtype, "out")
+            out = _empty(Q, shape, out_dtype, stream)
+        ob, oh = heads * D, D
     else:
         ot = _float_dtype(out.dtype, "out")
         if out.shape != shape or out.stride(2) != 1 or (out_dtype is not None and out.dtype != out_dtype):
             raise ValueError("out must have Q's shape, unit stride in the last axis and the output's dtype")
+        ob, oh, _ = out.stride()
+    lse_ptr, lse_stride = None, 0
     if lse is None:
         if want_lse:
             lse = _empty(cache.steps, (batch, heads), torch.float32, stream)
-    elif lse.dtype != torch.float32 or lse.shape != (batch, heads) or (heads > 1 and lse.stride(1) != 1):
-        raise ValueError("lse must be float32 (batch, query heads) with unit stride in the last axis")
+            lse_ptr, lse_stride = lse.data_ptr(), heads
+    else:
+        if lse.dtype is not torch.float32 or lse.shape != (batch, heads) or (heads > 1 and lse.stride(1) != 1):
+            raise ValueError("lse must be float32 (batch, query heads) with unit stride in the last axis")
+        lse_ptr, lse_stride = lse.data_ptr(), lse.stride(0)
     dev = _device(cache.k, Q, block_table, seq_lens, out, lse, workspace)
     need = imq_paged_attention_workspace(cache, batch, heads, max_len)
-    if workspace is None:
-        room = need
-        if need:
-            workspace = _empty(cache.k, (need,), torch.uint8, stream)
+    if workspace is not None:
+        room, room_ptr = workspace.numel() * workspace.element_size(), workspace.data_ptr()
+    elif need:
+        workspace = _empty(cache.k, need, torch.uint8, stream)
+        room, room_ptr = need, workspace.data_ptr()
     else:
-        room = workspace.numel() * workspace.element_size()
+        room, room_ptr = 0, None
     st = lib().imq_paged_attention(
-        cache._ref, Q.data_ptr(), qt, Q.stride(0), Q.stride(1), batch, heads, block_table.data_ptr(), block_table.stride(0),
-        width, seq_lens.data_ptr(), max_len, D ** -0.5 if scale is None else scale, out.data_ptr(), ot, out.stride(0),
-        out.stride(1), None if lse is None else lse.data_ptr(), 0 if lse is None else lse.stride(0),
-        None if workspace is None else workspace.data_ptr(), room, _raw_stream(stream, dev))
+        cache._ref, Q.data_ptr(), qt, stride[0], stride[1], batch, heads, block_table.data_ptr(), table_stride, width,
+        seq_lens.data_ptr(), max_len, D ** -0.5 if scale is None else scale, out.data_ptr(), ot, ob, oh, lse_ptr, lse_stride,
+        room_ptr, room, _raw_stream(stream, dev))
     if st:
         _check(st, "imq_paged_attention")
     return out, lse

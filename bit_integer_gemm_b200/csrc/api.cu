@@ -608,7 +608,7 @@ const char* imq_status_str(imq_status s) {
     case IMQ_ERR_CUDA: return "CUDA runtime error";
     case IMQ_ERR_UNSUPPORTED: return "unsupported input";
     case IMQ_ERR_PLAN: return "input not covered by the plan";
-    case IMQ_ERR_BOUNDS: return "plan index outside the plan's sizes (debug build)";
+    case IMQ_ERR_BOUNDS: return "index out of bounds (cache slot, page or length; plan index in the debug build)";
   }
   return "unknown status";
 }

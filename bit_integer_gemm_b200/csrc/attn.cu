@@ -258,7 +258,7 @@ struct Query {
       // a row of (almost) zeros, and one that is not finite (its scores' factor is NaN), have digits of 0
       const float top = __uint_as_float(key);
       const bool use = key_finite(key) && top > 1e-30f;
-      const float r = use ? __fdividef(kQMax, fminf(top, 8e37f)) : 0.f;  // (the division is approximate below 2^126)
+      const float r = use ? __fdividef(kQMax / 16.f, top * (1.f / 16.f)) : 0.f;  // (that division is 0 from 2^126 on)
       int32_t sum[3] = {};
 #pragma unroll
       for (int p = 0; p < kParts; ++p) {

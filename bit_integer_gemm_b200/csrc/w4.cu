@@ -594,7 +594,7 @@ int row_alignment(const void* p, int64_t row_bytes) {
 // What every call on a 4-bit weight checks.
 imq_status check_weight(const void* codes, int64_t ldc, const void* steps, int64_t lds, int64_t K, int64_t N, int32_t group) {
   if (K < 0 || N < 0 || (group != 32 && group != 64 && group != 128)) return IMQ_ERR_ARG;
-  if (K > INT32_MAX || N > INT32_MAX) return IMQ_ERR_UNSUPPORTED;
+  if (K > (1 << 30) || N > (1 << 30)) return IMQ_ERR_UNSUPPORTED;
   if (ldc < (K + kBlock - 1) / kBlock * kBlockBytes || ldc % 16 != 0 || lds < (K + group - 1) / group) return IMQ_ERR_ARG;
   if (K > 0 && N > 0 && (!codes || !steps || !aligned16(codes) || (reinterpret_cast<uintptr_t>(steps) & 3)))
     return IMQ_ERR_ARG;

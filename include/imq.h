@@ -55,7 +55,8 @@ typedef enum {
   IMQ_ERR_CUDA = 6,        /* a CUDA runtime call failed                                                 */
   IMQ_ERR_UNSUPPORTED = 7, /* legal input outside what the kernels implement (see imq_plan)             */
   IMQ_ERR_PLAN = 8,        /* imq_rtn_quantize_unpack: a quantised entry above the plan's max |A[:, t]| */
-  IMQ_ERR_BOUNDS = 9       /* debug build (IMQ_DEBUG) only: a plan index outside the plan's sizes        */
+  IMQ_ERR_BOUNDS = 9       /* a slot or page outside a cache, a sequence longer than the call covers;   */
+                           /* debug build (IMQ_DEBUG): a plan index outside the plan's sizes            */
 } imq_status;
 
 typedef enum { IMQ_F32 = 0, IMQ_BF16 = 1, IMQ_I16 = 2, IMQ_I32 = 3, IMQ_I64 = 4 } imq_dtype;
@@ -478,6 +479,7 @@ imq_status imq_unpacked_gemm_batched(int32_t batch, imq_plan_t *const *plans, co
  * Storage: code + 2^(bits-1).  At 8 bits a byte each.  At 4 bits eight consecutive codes per 32-bit word,
  * code e of the eight in bits 4 * (e / 2 + 4 * (e % 2)) .. + 3.
  * All calls are asynchronous and allocate nothing; argument errors are returned at once and launch nothing.
+ * Make the first call on a device before capturing one into a graph (it sets the library up there).
  * Pointers must be aligned to their element type unless more is said.
  */
 
@@ -490,8 +492,8 @@ imq_status imq_unpacked_gemm_batched(int32_t batch, imq_plan_t *const *plans, co
  *         64 * ceil(K / IMQ_W4_BLOCK).  A row is blocks of IMQ_W4_BLOCK inputs, 64 bytes each: input r of a
  *         block is code r % 8 of word 4 * ((r % 32) / 8) + r / 32 of the block.  Inputs behind K are 0.
  * steps   device, fp32, N x ceil(K / group), leading dimension lds.
- * Errors: IMQ_ERR_ARG at once; IMQ_ERR_NONFINITE through the status word; IMQ_ERR_UNSUPPORTED for K or N of
- *         2^31 or more, or K above 8 million with transW = 0.
+ * Errors: IMQ_ERR_ARG at once; IMQ_ERR_NONFINITE through the status word; IMQ_ERR_UNSUPPORTED for K or N above
+ *         2^30, or K above 8 million with transW = 0.
  */
 #define IMQ_W4_BLOCK 128
 imq_status imq_w4_quantize(const void *W, imq_dtype wt, int64_t K, int64_t N, int64_t ldw, int32_t transW,

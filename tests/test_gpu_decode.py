@@ -460,6 +460,14 @@ def test_attention_of_very_small_and_large_values(imq, size):
     check_attention(imq, cache, q, table, n, scale=scale)
 
 
+def test_attention_of_queries_at_the_end_of_fp32(imq):
+    """Rows whose largest entries are 3.3e38, 2^126 and just beside it."""
+    cache, table, n = make_cache(imq, [70, 5, 33], 16, 1, 64, 4)
+    q = _randn(1, 3, 3, 64).clamp(-3, 3) / 3
+    q = q / q.abs().amax(-1, keepdim=True) * torch.tensor([3.3e38, 2.0 ** 126, 8.4e37], device="cuda")[None, :, None]
+    check_attention(imq, cache, q, table, n, scale=1e-37)
+
+
 def test_attention_of_steps_of_very_different_sizes(imq):
     """Values that grow a millionfold from token to token: the sums' unit grows with them."""
     H, D, page, n = 1, 64, 16, 200
@@ -496,6 +504,41 @@ def test_attention_of_sequences_that_share_pages(imq):
     """One prefix on the same pages, read by several sequences of several lengths."""
     cache, table, n = make_cache(imq, [500], 32, 2, 128, 4)
     check_attention(imq, cache, _randn(1, 4, 4, 128), table.expand(4, -1), torch.tensor([500, 100, 31, 499], dtype=torch.int32, device="cuda"))
+
+
+def test_attention_of_many_short_sequences(imq):
+    """More sequences than the device holds CTAs, a quarter of them empty."""
+    lens = [(7 * i) % 41 if i % 4 else 0 for i in range(1100)]
+    cache, table, n = make_cache(imq, lens, 16, 1, 64, 4)
+    check_attention(imq, cache, _randn(1, len(lens), 2, 64), table, n)
+
+
+@pytest.mark.parametrize("H,L,bits", [(32, 40000, 4), (30, 36001, 8)])
+def test_attention_of_long_parts(imq, H, L, bits):
+    """So many tokens and heads that a warp takes more than 32 runs of one row; page numbers are read in batches."""
+    cache, table, n = make_cache(imq, [L], 48, H, 64, bits, poison=False)
+    check_attention(imq, cache, _randn(1, 1, H, 64), table, n)
+
+
+def test_two_graphs_replayed_at_once(imq):
+    """Each with a workspace of its own."""
+    cache, table, n = make_cache(imq, [3000, 0, 5000], 64, 2, 128, 8)
+    Qs = [_randn(i, 3, 8, 128) for i in range(2)]
+    want = [imq.imq_paged_attention(cache, q, table, n) for q in Qs]
+    graphs, got, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for q in Qs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(imq.imq_paged_attention(cache, q, table, n))
+        graphs.append(g)
+    for _ in range(10):
+        for (o, l), g, s in zip(got, graphs, streams):
+            with torch.cuda.stream(s):
+                o.zero_(), l.zero_()
+                g.replay()
+        torch.cuda.synchronize()
+        for (o, l), (wo, wl) in zip(got, want):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
 
 
 def test_attention_does_not_depend_on_the_bound_or_the_workspace(imq):
