@@ -17,12 +17,15 @@ struct VecArgs {
   int64_t n, k_tok, k_head, v_tok, v_head;
   const int64_t* slots;
   int aligned;
+  int head_shift, page_shift;  // heads = 2^head_shift, page_size = 2^page_shift, or -1
   int32_t* status;
   uint32_t one;  // kOneF16
 };
 
-// Tokens a lane group takes: their loads are under way together.
-constexpr int kTokens = 2;
+// Tokens a lane group takes, their loads under way together: four where that still fills the SMs twice (8191 tokens of 8
+// heads at 4 bits, written: 18.7 us with two, 15.6 with four), one below (32 tokens of 32 heads, written and read
+// back: 7.2 us with four, 4.7 with two).
+constexpr int kManyTokens = 4;
 
 // The cache place of a token's vector: page, and vector within the page's head block.  False for a token that is skipped.
 __device__ __forceinline__ bool locate(const VecArgs& a, int64_t tok, int head, bool report, uint32_t* page, int64_t* at) {
@@ -34,7 +37,8 @@ __device__ __forceinline__ bool locate(const VecArgs& a, int64_t tok, int head, 
   }
   uint32_t p, place;
   if (slot <= UINT32_MAX) {
-    p = (uint32_t)slot / (uint32_t)a.c.page_size, place = (uint32_t)slot - p * (uint32_t)a.c.page_size;
+    p = a.page_shift >= 0 ? (uint32_t)slot >> a.page_shift : (uint32_t)slot / (uint32_t)a.c.page_size;
+    place = (uint32_t)slot - p * (uint32_t)a.c.page_size;
   } else {
     p = (uint32_t)(slot / a.c.page_size), place = (uint32_t)(slot % a.c.page_size);
   }
@@ -43,15 +47,49 @@ __device__ __forceinline__ bool locate(const VecArgs& a, int64_t tok, int head, 
   return true;
 }
 
+// Eight entries as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void load_vec(const T* p, bool vec, float (&x)[8]) {
-  if (vec) {
-    load8(p, x);
-  } else {
+struct Raw {
+  static constexpr int kWords = 2 * sizeof(T);
+  uint32_t w[kWords];
+
+  __device__ __forceinline__ void load(const T* p, bool vec) {
+    if (vec) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = to_f32(p[e]);
+      for (int q = 0; q < kWords / 4; ++q) {
+        const uint4 v = reinterpret_cast<const uint4*>(p)[q];
+        w[4 * q] = v.x, w[4 * q + 1] = v.y, w[4 * q + 2] = v.z, w[4 * q + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if constexpr (sizeof(T) == 4) w[e] = __float_as_uint(p[e]);
+        else if (e % 2 == 0) w[e / 2] = __bfloat16_as_ushort(p[e]) | (uint32_t)__bfloat16_as_ushort(p[e + 1]) << 16;
+      }
+    }
   }
-}
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ float entry(int e) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
+    else return __uint_as_float(e % 2 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
+  }
+  // abs_key of the largest entry; two bf16 entries are compared at a time
+  __device__ __forceinline__ uint32_t key() const {
+    uint32_t m = 0;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+      return m;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+      return max(m << 16, m & 0xFFFF0000u);
+    }
+  }
+};
 // 16 bytes.
 __device__ __forceinline__ void store_vec(__nv_bfloat16* p, bool vec, const float (&x)[8]) {
   if (vec) {
@@ -71,70 +109,79 @@ __device__ __forceinline__ void store_vec(float* p, bool vec, const float (&x)[4
 }
 
 // kLanes: lanes of a vector's group (a power of two >= D / 8; the lanes at and above D / 8 hold zeros).
-template <typename T, int kBits, int kLanes>
+template <typename T, int kBits, int kLanes, int kTokens>
 __global__ void __launch_bounds__(256) k_kv_write(const __grid_constant__ VecArgs a) {
   const imq_kv_cache& c = a.c;
   const int i = threadIdx.x % kLanes, vec_bytes = c.head_dim * kBits / 8;
   const uint32_t unit = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
-  const int64_t tok0 = (int64_t)(unit / (uint32_t)c.n_heads) * kTokens;
-  const int head = unit % (uint32_t)c.n_heads;
+  const uint32_t set = a.head_shift >= 0 ? unit >> a.head_shift : unit / (uint32_t)c.n_heads;
+  const int64_t tok0 = (int64_t)set * kTokens;
+  const int head = unit - set * (uint32_t)c.n_heads;
   const bool lane = 8 * i < c.head_dim;
-  float k[kTokens][8] = {}, v[kTokens][8] = {};
+  Raw<T> k[kTokens], v[kTokens];
+  const T* const kp0 = static_cast<const T*>(a.K) + tok0 * a.k_tok + head * a.k_head + 8 * i;
+  const T* const vp0 = static_cast<const T*>(a.V) + tok0 * a.v_tok + head * a.v_head + 8 * i;
+#pragma unroll
+  for (int j = 0; j < kTokens; ++j) {
+    if (lane && tok0 + j < a.n) k[j].load(kp0 + j * a.k_tok, a.aligned), v[j].load(vp0 + j * a.v_tok, a.aligned);
+    else k[j].clear(), v[j].clear();
+  }
   uint32_t page[kTokens];
   int64_t at[kTokens];
   bool on[kTokens];
 #pragma unroll
-  for (int j = 0; j < kTokens; ++j)
-    if (lane && tok0 + j < a.n) {
-      load_vec(static_cast<const T*>(a.K) + (tok0 + j) * a.k_tok + head * a.k_head + 8 * i, a.aligned, k[j]);
-      load_vec(static_cast<const T*>(a.V) + (tok0 + j) * a.v_tok + head * a.v_head + 8 * i, a.aligned, v[j]);
-    }
-#pragma unroll
   for (int j = 0; j < kTokens; ++j) on[j] = locate(a, tok0 + j, head, i == 0, &page[j], &at[j]);
-  uint32_t key[4] = {};  // of the first token's key and value, and the second's
+  uint32_t key[2][kTokens];
 #pragma unroll
-  for (int j = 0; j < kTokens; ++j)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      key[2 * j] = max(key[2 * j], abs_key(k[j][e]));
-      key[2 * j + 1] = max(key[2 * j + 1], abs_key(v[j][e]));
-    }
+  for (int j = 0; j < kTokens; ++j) key[0][j] = k[j].key(), key[1][j] = v[j].key();
 #pragma unroll
   for (int o = 1; o < kLanes; o <<= 1)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) key[q] = max(key[q], __shfl_xor_sync(0xffffffffu, key[q], o));
-  float s[4], step[4];
-  four_scales(key, (float)((1 << (kBits - 1)) - 1), s, step);
+    for (int q = 0; q < 2 * kTokens; ++q)
+      key[q / kTokens][q % kTokens] = max(key[q / kTokens][q % kTokens], __shfl_xor_sync(0xffffffffu, key[q / kTokens][q % kTokens], o));
+  float s[2][kTokens], step[2][kTokens];
+  constexpr float kBeta = (float)((1 << (kBits - 1)) - 1);
+  if constexpr (kTokens == 4) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) four_scales(key[q], kBeta, s[q], step[q]);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) group_scale(key[q][0], kBeta, &s[q][0], &step[q][0]);
+  }
 #pragma unroll
   for (int j = 0; j < kTokens; ++j) {
     if (!lane || !on[j]) continue;
     uint8_t* kp = c.k + page[j] * c.k_page_stride + at[j] * vec_bytes + kBits * i;  // eight codes are kBits bytes
     uint8_t* vp = c.v + page[j] * c.v_page_stride + at[j] * vec_bytes + kBits * i;
-    const float ks = s[2 * j], vs = s[2 * j + 1];
-    if constexpr (kBits == 4) {
-      *reinterpret_cast<uint32_t*>(kp) = pack4(k[j], ks);
-      *reinterpret_cast<uint32_t*>(vp) = pack4(v[j], vs);
-    } else {
-      *reinterpret_cast<uint2*>(kp) = make_uint2(pack8(k[j][0], k[j][1], k[j][2], k[j][3], ks), pack8(k[j][4], k[j][5], k[j][6], k[j][7], ks));
-      *reinterpret_cast<uint2*>(vp) = make_uint2(pack8(v[j][0], v[j][1], v[j][2], v[j][3], vs), pack8(v[j][4], v[j][5], v[j][6], v[j][7], vs));
+    float x[8];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const Raw<T>& r = q ? v[j] : k[j];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = r.entry(e);
+      if constexpr (kBits == 4)
+        *reinterpret_cast<uint32_t*>(q ? vp : kp) = pack4(x, s[q][j]);
+      else
+        *reinterpret_cast<uint2*>(q ? vp : kp) = make_uint2(pack8(x[0], x[1], x[2], x[3], s[q][j]), pack8(x[4], x[5], x[6], x[7], s[q][j]));
     }
     if (i == 0) {
-      *reinterpret_cast<float2*>(c.steps + page[j] * c.steps_page_stride + at[j] * 2) = make_float2(step[2 * j], step[2 * j + 1]);
-      if (!key_finite(key[2 * j]) || !key_finite(key[2 * j + 1])) set_status(a.status, IMQ_ERR_NONFINITE);
+      *reinterpret_cast<float2*>(c.steps + page[j] * c.steps_page_stride + at[j] * 2) = make_float2(step[0][j], step[1][j]);
+      if (!key_finite(key[0][j]) || !key_finite(key[1][j])) set_status(a.status, IMQ_ERR_NONFINITE);
     }
   }
 }
 
 // A lane makes 16 bytes of a vector: 8 entries of bf16, 4 of fp32 (so that a warp's stores are one piece).  kLanes: a power
 // of two that covers a vector.
-template <typename T, int kBits, int kLanes>
+template <typename T, int kBits, int kLanes, int kTokens>
 __global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ VecArgs a) {
   constexpr int kMine = 16 / sizeof(T), kWords = kMine * kBits > 32 ? 2 : 1;
   const imq_kv_cache& c = a.c;
   const int i = threadIdx.x % kLanes, vec_bytes = c.head_dim * kBits / 8;
   const uint32_t unit = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
-  const int64_t tok0 = (int64_t)(unit / (uint32_t)c.n_heads) * kTokens;
-  const int head = unit % (uint32_t)c.n_heads;
+  const uint32_t set = a.head_shift >= 0 ? unit >> a.head_shift : unit / (uint32_t)c.n_heads;
+  const int64_t tok0 = (int64_t)set * kTokens;
+  const int head = unit - set * (uint32_t)c.n_heads;
   // the word (or two) of this lane's codes; at 4 bits and fp32 two lanes share a word
   const int from = i * kMine * kBits / 32 * 4;
   uint32_t kw[kTokens][kWords], vw[kTokens][kWords];
@@ -181,22 +228,30 @@ __global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ VecArgs
   }
 }
 
-template <typename T, int kBits>
-void run(bool write, const VecArgs& a, cudaStream_t st) {
-  const int mine = write ? 8 : 16 / (int)sizeof(T), need = a.c.head_dim / mine;
-  const int lanes = need <= 8 ? 8 : need <= 16 ? 16 : need <= 32 ? 32 : 64;
+int log2_or(int32_t n) { return (n & (n - 1)) == 0 ? __builtin_ctz(n) : -1; }
+
+template <typename T, int kBits, int kTokens>
+void run_tokens(bool write, const VecArgs& a, int lanes, cudaStream_t st) {
   const int64_t units = (a.n + kTokens - 1) / kTokens * a.c.n_heads;
   const unsigned ctas = (unsigned)((units + 256 / lanes - 1) / (256 / lanes));
   if (write) {
-    if (lanes == 8) k_kv_write<T, kBits, 8><<<ctas, 256, 0, st>>>(a);
-    if (lanes == 16) k_kv_write<T, kBits, 16><<<ctas, 256, 0, st>>>(a);
-    if (lanes == 32) k_kv_write<T, kBits, 32><<<ctas, 256, 0, st>>>(a);
+    if (lanes == 8) k_kv_write<T, kBits, 8, kTokens><<<ctas, 256, 0, st>>>(a);
+    if (lanes == 16) k_kv_write<T, kBits, 16, kTokens><<<ctas, 256, 0, st>>>(a);
+    if (lanes == 32) k_kv_write<T, kBits, 32, kTokens><<<ctas, 256, 0, st>>>(a);
   } else {
-    if (lanes == 8) k_kv_read<T, kBits, 8><<<ctas, 256, 0, st>>>(a);
-    if (lanes == 16) k_kv_read<T, kBits, 16><<<ctas, 256, 0, st>>>(a);
-    if (lanes == 32) k_kv_read<T, kBits, 32><<<ctas, 256, 0, st>>>(a);
-    if (lanes == 64) k_kv_read<T, kBits, 64><<<ctas, 256, 0, st>>>(a);
+    if (lanes == 8) k_kv_read<T, kBits, 8, kTokens><<<ctas, 256, 0, st>>>(a);
+    if (lanes == 16) k_kv_read<T, kBits, 16, kTokens><<<ctas, 256, 0, st>>>(a);
+    if (lanes == 32) k_kv_read<T, kBits, 32, kTokens><<<ctas, 256, 0, st>>>(a);
+    if (lanes == 64) k_kv_read<T, kBits, 64, kTokens><<<ctas, 256, 0, st>>>(a);
   }
+}
+
+template <typename T, int kBits>
+void run(bool write, const VecArgs& a, int num_sms, cudaStream_t st) {
+  const int mine = write ? 8 : 16 / (int)sizeof(T), need = a.c.head_dim / mine;
+  const int lanes = need <= 8 ? 8 : need <= 16 ? 16 : need <= 32 ? 32 : 64;
+  if (a.n * a.c.n_heads * lanes >= (int64_t)kManyTokens * 2 * 256 * num_sms) run_tokens<T, kBits, kManyTokens>(write, a, lanes, st);
+  else run_tokens<T, kBits, 1>(write, a, lanes, st);
 }
 
 imq_status launch(bool write, const imq_kv_cache* cache, void* K, int64_t k_tok, int64_t k_head, void* V, int64_t v_tok,
@@ -215,13 +270,14 @@ imq_status launch(bool write, const imq_kv_cache* cache, void* K, int64_t k_tok,
   s = device_state(&ds);
   if (s != IMQ_OK) return s;
   const int64_t strides = ((K ? k_tok | k_head : 0) | (V ? v_tok | v_head : 0)) * size;
-  VecArgs a{*cache, K, V, n, k_tok, k_head, v_tok, v_head, slots, ((kp | vp | (uintptr_t)strides) & 15) == 0, ds->status, kOneF16};
+  VecArgs a{*cache, K, V, n, k_tok, k_head, v_tok, v_head, slots, ((kp | vp | (uintptr_t)strides) & 15) == 0,
+            log2_or(cache->n_heads), log2_or(cache->page_size), ds->status, kOneF16};
   if (t == IMQ_F32) {
-    if (cache->bits == 4) run<float, 4>(write, a, st);
-    else run<float, 8>(write, a, st);
+    if (cache->bits == 4) run<float, 4>(write, a, ds->num_sms, st);
+    else run<float, 8>(write, a, ds->num_sms, st);
   } else {
-    if (cache->bits == 4) run<__nv_bfloat16, 4>(write, a, st);
-    else run<__nv_bfloat16, 8>(write, a, st);
+    if (cache->bits == 4) run<__nv_bfloat16, 4>(write, a, ds->num_sms, st);
+    else run<__nv_bfloat16, 8>(write, a, ds->num_sms, st);
   }
   return cudaGetLastError() == cudaSuccess ? IMQ_OK : IMQ_ERR_CUDA;
 }

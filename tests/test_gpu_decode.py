@@ -243,7 +243,7 @@ def cache_values(cache):
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("D", [64, 128, 192, 256])
-@pytest.mark.parametrize("n,H,page", [(1, 1, 16), (5, 3, 16), (77, 2, 48), (300, 8, 64)])
+@pytest.mark.parametrize("n,H,page", [(1, 1, 16), (5, 3, 16), (77, 2, 48), (300, 8, 64), (5003, 9, 48), (5003, 8, 64)])
 def test_cache_write_and_read(imq, n, H, page, D, bits, dtype):
     pages = -(-n // page) + 3
     cache = imq.KVCache.zeros(pages, page, H, D, bits)
