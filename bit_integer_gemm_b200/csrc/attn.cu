@@ -24,11 +24,14 @@
 //
 // The softmax keeps a reference instead of the running maximum: it is raised (and the sums rescaled) only when a
 // weight exceeds it 8 times, or a value's step the unit of steps twice (together the room that fp16 leaves above
-// 2^11), so most tiles need no exchange between lanes.
+// 2^11), so most runs need no exchange between lanes.
 //
 // Split: the work of all sequences and key heads lies in one line of units of 64 tokens, cut into equal parts, one
-// for each CTA that the SMs hold at once; so lengths may differ as they will.  A CTA's four warps take runs
-// of 16 tokens in turn, each with its own ring of asynchronous copies (so that a tile waits for no barrier but
+// for each CTA that the SMs hold at once; so lengths may differ as they will.  A row (one sequence's tokens of one key
+// head) counts four units more than it has, for its queries and its end: without them a CTA whose part is made of many
+// short rows came last (64 sequences of 1 to 4097 tokens, 8 key heads of 64: 47.2 us, with them 32.6; 16 of up to 8192
+// at 4 bits: 37.0 and 29.0; 2 or 6 to 12 instead of four: 32.6 to 36.2 and 29.4 to 31.0).  A CTA's four warps take runs
+// of 16 tokens in turn, each with its own ring of asynchronous copies (so that a run waits for no barrier but
 // the warp's), and join in shared memory.  Rows that several CTAs
 // share join in k_attn_join from partial sums in the workspace, in a fixed order.
 #include <atomic>
@@ -43,6 +46,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kRun = 16;              // tokens that a warp copies at a time; they lie in one page (pages are multiples of it)
 constexpr int kUnit = kWarps * kRun;  // tokens: the grain of the split
+constexpr uint32_t kRowCost = 4;      // what a row costs besides its units, in units
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 3.f;          // how far, in powers of two, a weight may exceed the reference's,
 constexpr float kStepSlack = 2.f;      // and how many times a step the unit of steps
@@ -180,7 +184,12 @@ __device__ __forceinline__ float quiet_nan() { return __uint_as_float(0x7FC00000
 __device__ __forceinline__ uint32_t units_of(const AttnArgs& a, int len) {
   return len <= 0 || len > a.limit ? 0u : (uint32_t)(len + kUnit - 1) / kUnit;
 }
-// The parts of the line: `all` units over `n` CTAs, the first all % n take one more.
+// A row's length in the line: its units, behind kRowCost places that stand for its start and end.
+__device__ __forceinline__ uint32_t cost_of(const AttnArgs& a, int len) {
+  const uint32_t n = units_of(a, len);
+  return n ? n + kRowCost : 0u;
+}
+// The parts of the line: `all` places over `n` CTAs, the first all % n take one more.
 struct Parts {
   uint32_t each, more;
   __device__ __forceinline__ Parts(uint32_t all, uint32_t n) : each(all / n), more(all % n) {}
@@ -208,13 +217,12 @@ struct Shape {
   static constexpr int kCols = kD / 8;                 // 8-column blocks of p * v
   static constexpr int kValues = 16 * kRow, kStepsAt = kValues + 16 * kPitch;
   static constexpr int kRunBytes = kStepsAt + 128;     // keys, values, steps of 16 tokens
-  // A tile is two runs where registers and shared memory allow: their chains of dependent instructions overlap.
-  static constexpr int kRuns = 1;
-  static constexpr int kTileBytes = kRuns * kRunBytes;
-  static constexpr int kBudget = 13000;  // of a warp's ring: three CTAs an SM have about 100 KB of copies under way
-  static constexpr int kStages = kBudget / kTileBytes < 2 ? 2 : kBudget / kTileBytes > 8 ? 8 : kBudget / kTileBytes;
-  static constexpr int kRing = kStages * kTileBytes;
-  static constexpr int kPerSm = kD <= 64 ? 4 : kD <= 128 ? 3 : 2;     // CTAs an SM, by the registers of the sums
+  // about 13 KB for a warp's ring: three CTAs an SM have about 100 KB of copies under way
+  static constexpr int kStages = 13000 / kRunBytes < 2 ? 2 : 13000 / kRunBytes > 8 ? 8 : 13000 / kRunBytes;
+  static constexpr int kRing = kStages * kRunBytes;
+  // CTAs an SM, by the registers of the sums.  At 128 a fourth would cost spills: three take 52 us for 131072 tokens of
+  // 8 key heads at 8 bits, four 55.
+  static constexpr int kPerSm = kD <= 64 ? 4 : kD <= 128 ? 3 : 2;
   static constexpr int kHeads = 8 * kM;
   static constexpr int kQOps = kM + 1;                 // operands of the digits, 512 bytes each a step
   static constexpr int kQBytes = kSteps * kQOps * 512;
@@ -309,7 +317,7 @@ template <int kBits, int kD, int kM>
 __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_attn(const __grid_constant__ AttnArgs a) {
   using S = Shape<kBits, kD, kM>;
   using KP = typename S::KP;
-  constexpr int kStages = S::kStages, kRow = S::kRow, kRuns = S::kRuns;
+  constexpr int kStages = S::kStages, kRow = S::kRow;
   extern __shared__ __align__(16) uint8_t smem[];
   uint4* const qs = reinterpret_cast<uint4*>(smem);
   uint8_t* const ring = smem + S::kQBytes;
@@ -336,14 +344,14 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
         a.lse[b * a.lse_batch + i] = over ? quiet_nan() : minus_inf();
   }
 
-  // ---- the first warp keeps the CTA's place in the line: units u0 .. u1 - 1, the sequence b that u0 lies in, and the
-  // units before it
+  // ---- the first warp keeps the CTA's part of the line, u0 .. u1 - 1, the sequence that u0 lies in, and the places before
+  // that
   uint32_t u0 = 0, u1 = 0, base = 0;
   int b_now = 0;
   const uint32_t rows = a.c.n_heads * a.head_chunks;
   if (warp == 0) {
-    // inclusive sums of the first 32 sequences' units, and the sum of all
-    const uint32_t mine = lane < a.batch ? units_of(a, __ldg(a.lens + lane)) * rows : 0u;
+    // inclusive sums of the first 32 sequences' places, and the sum of all
+    const uint32_t mine = lane < a.batch ? cost_of(a, __ldg(a.lens + lane)) * rows : 0u;
     uint32_t sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -353,7 +361,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
     uint32_t all = __shfl_sync(0xffffffffu, sum, 31);
     if (a.batch > 32) {
       uint32_t more = 0;
-      for (int i = 32 + lane; i < a.batch; i += 32) more += units_of(a, __ldg(a.lens + i));
+      for (int i = 32 + lane; i < a.batch; i += 32) more += cost_of(a, __ldg(a.lens + i));
       all += __reduce_add_sync(0xffffffffu, more) * rows;
     }
     const uint32_t ctas = min((uint32_t)a.ctas, all);
@@ -371,7 +379,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
         }
         base += __shfl_sync(0xffffffffu, sum, 31);
         b_now += 32;
-        own = b_now + lane < a.batch ? units_of(a, __ldg(a.lens + b_now + lane)) * rows : 0u;
+        own = b_now + lane < a.batch ? cost_of(a, __ldg(a.lens + b_now + lane)) * rows : 0u;
         sum = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -387,16 +395,20 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
     if (warp == 0) {
       uint32_t take = 0, per_row = 0, row = 0, unit = 0;
       int len = 0;
-      if (u0 < u1) {
-        for (;;) {
-          len = __ldg(a.lens + b_now);
-          per_row = units_of(a, len);
-          if (u0 - base < per_row * rows) break;
-          base += per_row * rows;
+      while (u0 < u1 && take == 0) {
+        len = __ldg(a.lens + b_now);
+        const uint32_t cost = cost_of(a, len);
+        if (u0 - base >= cost * rows) {
+          base += cost * rows;
           ++b_now;
+          continue;
         }
-        row = (u0 - base) / per_row, unit = (u0 - base) - row * per_row, take = min(per_row - unit, u1 - u0);
-        u0 += take;
+        per_row = units_of(a, len);
+        row = (u0 - base) / cost;
+        const uint32_t at = (u0 - base) - row * cost, to = min(cost, at + (u1 - u0));  // this CTA's places of the row
+        unit = at > kRowCost ? at - kRowCost : 0u;
+        take = to > kRowCost ? to - kRowCost - unit : 0u;
+        u0 += to - at;
       }
       if (lane == 0) {
         *reinterpret_cast<int4*>(s_part) = make_int4(b_now, (int)row, (int)unit, (int)take);
@@ -444,60 +456,57 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
     // ---- the warp's copies
     const uint32_t mine = smem_addr(ring) + warp * S::kRing;
     bool bad = false;
-    uint32_t fill = mine;  // the tile that is filled next
-    auto issue = [&](int i) {
-      if (i * kRuns < n_runs) {
-#pragma unroll
-        for (int r = 0; r < kRuns; ++r) {
-          const int u = i * kRuns + r, left = end - (first + u * kUnit);
-          if (r == 0 && (u & 31) == 0 && u > 0) {
-            now = next;
-            next = locate(u + 32);
-          }
-          const uint32_t ko = __shfl_sync(0xffffffffu, now.k, u & 31), vo = __shfl_sync(0xffffffffu, now.v, u & 31);
-          const uint32_t so = __shfl_sync(0xffffffffu, now.s, u & 31);
-          const uint8_t* const kp = a.c.k + (uint64_t)ko * 16 + (g * kRow + c * 16);
-          const uint8_t* const vp = a.c.v + (uint64_t)vo * 16 + lane * 16;
-          const uint8_t* const sp = reinterpret_cast<const uint8_t*>(a.c.steps) + (uint64_t)so * 16 + lane * 16;
-          const uint32_t to = fill + r * S::kRunBytes, to16 = to + lane * 16, to8 = to + lane * 8 + KP::n16 * 512;
-          if (left >= kRun && ko != kNowhere) {
-            // keys: tokens g and g + 8, this lane's quarter; values: the run's bytes in order
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-#pragma unroll
-              for (int q = 0; q < KP::n16; ++q) cp_async<16>(to16 + j * 8 * kRow + q * 512, kp + j * 8 * kRow + q * 64);
-              if (KP::n8) cp_async<8>(to8 + j * 8 * kRow, kp - 8 * c + j * 8 * kRow + 64 * KP::n16);
-            }
-#pragma unroll
-            for (int q = 0; q < S::kChunks / 2; ++q) {
-              const int at = q * 32 + lane;
-              cp_async<16>(to + S::kValues + S::chunk_at(at / S::kChunks, at % S::kChunks), vp + q * 512);
-            }
-            if (lane < 8) cp_async<16>(to16 + S::kStepsAt, sp);
-          } else {
-            // the end of the sequence, or a page outside the cache: what is not read is zero-filled (steps of 0: no
-            // stale value meets a weight of 0), with an address that is not read either
-            const int valid = ko == kNowhere ? 0 : min(max(left, 0), kRun);
-            bad |= ko == kNowhere && left > 0;
-#pragma unroll 1
-            for (int j = 0; j < 2; ++j) {
-              const bool on = 8 * j + g < valid;
-              const uint8_t* from = on ? kp + j * 8 * kRow : a.c.k;
-#pragma unroll
-              for (int q = 0; q < KP::n16; ++q) cp_async_part<16>(to16 + j * 8 * kRow + q * 512, from + (on ? q * 64 : 0), on ? 16u : 0u);
-              if (KP::n8) cp_async_part<8>(to8 + j * 8 * kRow, from + (on ? 64 * KP::n16 - 8 * c : 0), on ? 8u : 0u);
-            }
-#pragma unroll 1
-            for (int q = 0; q < S::kChunks / 2; ++q) {
-              const int at = q * 32 + lane;
-              const bool on = at / S::kChunks < valid;
-              cp_async_part<16>(to + S::kValues + S::chunk_at(at / S::kChunks, at % S::kChunks), on ? vp + q * 512 : a.c.v, on ? 16u : 0u);
-            }
-            const int n = min(max(valid - 2 * lane, 0), 2);
-            if (lane < 8) cp_async_part<16>(to16 + S::kStepsAt, n ? sp : reinterpret_cast<const uint8_t*>(a.c.steps), 8u * n);
-          }
+    uint32_t fill = mine;  // the stage that is filled next
+    auto issue = [&](int u) {
+      if (u < n_runs) {
+        const int left = end - (first + u * kUnit);
+        if ((u & 31) == 0 && u > 0) {
+          now = next;
+          next = locate(u + 32);
         }
-        fill = fill + S::kTileBytes == mine + S::kRing ? mine : fill + S::kTileBytes;
+        const uint32_t ko = __shfl_sync(0xffffffffu, now.k, u & 31), vo = __shfl_sync(0xffffffffu, now.v, u & 31);
+        const uint32_t so = __shfl_sync(0xffffffffu, now.s, u & 31);
+        const uint8_t* const kp = a.c.k + (uint64_t)ko * 16 + (g * kRow + c * 16);
+        const uint8_t* const vp = a.c.v + (uint64_t)vo * 16 + lane * 16;
+        const uint8_t* const sp = reinterpret_cast<const uint8_t*>(a.c.steps) + (uint64_t)so * 16 + lane * 16;
+        const uint32_t to16 = fill + lane * 16, to8 = fill + lane * 8 + KP::n16 * 512;
+        if (left >= kRun && ko != kNowhere) {
+          // keys: tokens g and g + 8, this lane's quarter; values: the run's bytes in order
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int q = 0; q < KP::n16; ++q) cp_async<16>(to16 + j * 8 * kRow + q * 512, kp + j * 8 * kRow + q * 64);
+            if (KP::n8) cp_async<8>(to8 + j * 8 * kRow, kp - 8 * c + j * 8 * kRow + 64 * KP::n16);
+          }
+#pragma unroll
+          for (int q = 0; q < S::kChunks / 2; ++q) {
+            const int at = q * 32 + lane;
+            cp_async<16>(fill + S::kValues + S::chunk_at(at / S::kChunks, at % S::kChunks), vp + q * 512);
+          }
+          if (lane < 8) cp_async<16>(to16 + S::kStepsAt, sp);
+        } else {
+          // the end of the sequence, or a page outside the cache: what is not read is zero-filled (steps of 0: no
+          // stale value meets a weight of 0), with an address that is not read either
+          const int valid = ko == kNowhere ? 0 : min(left, kRun);
+          bad |= ko == kNowhere;
+#pragma unroll 1
+          for (int j = 0; j < 2; ++j) {
+            const bool on = 8 * j + g < valid;
+            const uint8_t* from = on ? kp + j * 8 * kRow : a.c.k;
+#pragma unroll
+            for (int q = 0; q < KP::n16; ++q) cp_async_part<16>(to16 + j * 8 * kRow + q * 512, from + (on ? q * 64 : 0), on ? 16u : 0u);
+            if (KP::n8) cp_async_part<8>(to8 + j * 8 * kRow, from + (on ? 64 * KP::n16 - 8 * c : 0), on ? 8u : 0u);
+          }
+#pragma unroll 1
+          for (int q = 0; q < S::kChunks / 2; ++q) {
+            const int at = q * 32 + lane;
+            const bool on = at / S::kChunks < valid;
+            cp_async_part<16>(fill + S::kValues + S::chunk_at(at / S::kChunks, at % S::kChunks), on ? vp + q * 512 : a.c.v, on ? 16u : 0u);
+          }
+          const int n = min(max(valid - 2 * lane, 0), 2);
+          if (lane < 8) cp_async_part<16>(to16 + S::kStepsAt, n ? sp : reinterpret_cast<const uint8_t*>(a.c.steps), 8u * n);
+        }
+        fill = fill + S::kRunBytes == mine + S::kRing ? mine : fill + S::kRunBytes;
       }
       cp_async_commit();
     };
@@ -523,34 +532,33 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
       for (int i = 0; i < S::kSteps * S::kQOps; ++i) qr[i] = qs[i * 32 + lane];
     }
 
-    // ---- the warp's tiles
+    // ---- the warp's runs
     float o[S::kCols][4] = {};
     float m[kM], l[kM], vref = kStepFloor, winv = kPScale / kStepFloor;
 #pragma unroll
     for (int r = 0; r < kM; ++r) m[r] = minus_inf(), l[r] = 0.f;
-    const uint8_t* tile = ring + warp * S::kRing;
+    const uint8_t* run = ring + warp * S::kRing;
 
 #pragma unroll 1
-    for (int i = 0; i * kRuns < n_runs; ++i) {
+    for (int u = 0; u < n_runs; ++u) {
       cp_async_wait<kStages - 2>();
-      __syncwarp();  // other lanes copied parts of the tile; and every lane is done with the tile that is overwritten now
-      issue(i + kStages - 1);
-      // ---- scores, two blocks of eight tokens a run; this lane's tokens of a run are 2c, 2c + 1, 2c + 8, 2c + 9, its
-      // heads g (and g + 8)
-      constexpr int kMine = 4 * kRuns;
+      __syncwarp();  // other lanes copied parts of the run; and every lane is done with the run that is overwritten now
+      issue(u + kStages - 1);
+      // ---- scores, two blocks of eight tokens; this lane's tokens are 2c, 2c + 1, 2c + 8, 2c + 9, its heads g (and g + 8)
+      constexpr int kMine = 4;
       float p[kM][kMine];
       {
-        int32_t acc[2 * kRuns][S::kQOps][4] = {};
-        uint32_t w[2 * kRuns][KP::kBytes / 4];
+        int32_t acc[2][S::kQOps][4] = {};
+        uint32_t w[2][KP::kBytes / 4];
 #pragma unroll
-        for (int j = 0; j < 2 * kRuns; ++j) read_pieces<KP>(tile + (j >> 1) * S::kRunBytes + (j & 1) * 8 * kRow, lane, w[j]);
+        for (int j = 0; j < 2; ++j) read_pieces<KP>(run + j * 8 * kRow, lane, w[j]);
 #pragma unroll
         for (int st = 0; st < S::kSteps; ++st) {
 #pragma unroll
           for (int op = 0; op < S::kQOps; ++op) {
             const uint4 q = kQInRegs ? qr[kQInRegs ? st * S::kQOps + op : 0] : qs[(st * S::kQOps + op) * 32 + lane];
 #pragma unroll
-            for (int j = 0; j < 2 * kRuns; ++j) {
+            for (int j = 0; j < 2; ++j) {
               const uint32_t b0 = kBits == 8 ? w[j][kBits == 8 ? 2 * st : 0] : w[j][kBits == 8 ? 0 : st] & 0x0F0F0F0Fu;
               const uint32_t b1 = kBits == 8 ? w[j][kBits == 8 ? 2 * st + 1 : 0] : w[j][kBits == 8 ? 0 : st] >> 4 & 0x0F0F0F0Fu;
               if (kM == 1 && op == 1) mma_s8u8(acc[j][op], q.x, 0u, q.z, 0u, b0, b1);  // rows 8-15 hold no digit
@@ -571,8 +579,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
       }
       float ks[kMine], vs[kMine];
 #pragma unroll
-      for (int j = 0; j < 2 * kRuns; ++j) {
-        const float4 st = *reinterpret_cast<const float4*>(tile + (j >> 1) * S::kRunBytes + S::kStepsAt + (j & 1) * 64 + c * 16);
+      for (int j = 0; j < 2; ++j) {
+        const float4 st = *reinterpret_cast<const float4*>(run + S::kStepsAt + j * 64 + c * 16);
         ks[2 * j] = st.x, vs[2 * j] = st.y, ks[2 * j + 1] = st.z, vs[2 * j + 1] = st.w;
       }
       float vmax = vs[0];
@@ -583,11 +591,11 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
       for (int r = 0; r < kM; ++r)
 #pragma unroll
         for (int j = 0; j < kMine; ++j) p[r][j] *= ks[j] * mul[r];
-      const int left = end - (first + i * kRuns * kUnit);  // run 1 of a tile lies kUnit tokens behind run 0
-      if (left < (kRuns - 1) * kUnit + kRun) {
+      const int left = end - (first + u * kUnit);
+      if (left < kRun) {
 #pragma unroll
         for (int j = 0; j < kMine; ++j)
-          if ((j >> 2) * kUnit + 8 * (j >> 1 & 1) + 2 * c + (j & 1) >= left) {
+          if (8 * (j >> 1) + 2 * c + (j & 1) >= left) {
 #pragma unroll
             for (int r = 0; r < kM; ++r) p[r][j] = minus_inf();
           }
@@ -616,7 +624,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
           l[r] *= alpha;
           fix[r] = alpha * ratio;
         }
-        if (i > 0) {
+        if (u > 0) {
 #pragma unroll
           for (int n = 0; n < S::kCols; ++n) {
             o[n][0] *= fix[0], o[n][1] *= fix[0];
@@ -634,43 +642,40 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
           p[r][j] *= vw;
         }
       }
+      uint32_t hi[kM][2], lo[kM][2];  // weights as operands
 #pragma unroll
-      for (int run = 0; run < kRuns; ++run) {
-        uint32_t hi[kM][2], lo[kM][2];  // weights as operands
-#pragma unroll
-        for (int r = 0; r < kM; ++r) {
-          split_f16(p[r][4 * run], p[r][4 * run + 1], &hi[r][0], &lo[r][0]);
-          split_f16(p[r][4 * run + 2], p[r][4 * run + 3], &hi[r][1], &lo[r][1]);
+      for (int r = 0; r < kM; ++r) {
+        split_f16(p[r][0], p[r][1], &hi[r][0], &lo[r][0]);
+        split_f16(p[r][2], p[r][3], &hi[r][1], &lo[r][1]);
+      }
+      auto product = [&](float (&acc)[4], uint32_t b0, uint32_t b1) {
+        if (kM == 1) {
+          mma_f16(acc, hi[0][0], lo[0][0], hi[0][1], lo[0][1], b0, b1);
+        } else {
+          mma_f16(acc, hi[0][0], hi[kM - 1][0], hi[0][1], hi[kM - 1][1], b0, b1);
+          mma_f16(acc, lo[0][0], lo[kM - 1][0], lo[0][1], lo[kM - 1][1], b0, b1);
         }
-        auto product = [&](float (&acc)[4], uint32_t b0, uint32_t b1) {
-          if (kM == 1) {
-            mma_f16(acc, hi[0][0], lo[0][0], hi[0][1], lo[0][1], b0, b1);
+      };
+#pragma unroll
+      for (int q = 0; q < S::kChunks; q += 2) {
+        // chunks q and q + 1 of tokens 0-7 and 8-15; a register holds two bytes (four nibbles) of tokens 2c and 2c + 1
+        uint32_t w[4];
+        ldmatrix_trans4(smem_addr(run) + S::kValues + S::chunk_at(lane % 16, q + lane / 16), w);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t x = w[2 * e], y = w[2 * e + 1];
+          if constexpr (kBits == 8) {
+            product(o[2 * (q + e)], bytes_f16(x, 0x5250, a.one), bytes_f16(y, 0x5250, a.one));
+            product(o[2 * (q + e) + 1], bytes_f16(x, 0x5351, a.one), bytes_f16(y, 0x5351, a.one));
           } else {
-            mma_f16(acc, hi[0][0], hi[kM - 1][0], hi[0][1], hi[kM - 1][1], b0, b1);
-            mma_f16(acc, lo[0][0], lo[kM - 1][0], lo[0][1], lo[kM - 1][1], b0, b1);
-          }
-        };
-#pragma unroll
-        for (int q = 0; q < S::kChunks; q += 2) {
-          // chunks q and q + 1 of tokens 0-7 and 8-15; a register holds two bytes (four nibbles) of tokens 2c and 2c + 1
-          uint32_t w[4];
-          ldmatrix_trans4(smem_addr(tile) + run * S::kRunBytes + S::kValues + S::chunk_at(lane % 16, q + lane / 16), w);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t x = w[2 * e], y = w[2 * e + 1];
-            if constexpr (kBits == 8) {
-              product(o[2 * (q + e)], bytes_f16(x, 0x5250, a.one), bytes_f16(y, 0x5250, a.one));
-              product(o[2 * (q + e) + 1], bytes_f16(x, 0x5351, a.one), bytes_f16(y, 0x5351, a.one));
-            } else {
-              product(o[4 * (q + e)], nibbles_f16<false>(x, a.one), nibbles_f16<false>(y, a.one));
-              product(o[4 * (q + e) + 1], nibbles_f16<true>(x, a.one), nibbles_f16<true>(y, a.one));
-              product(o[4 * (q + e) + 2], nibbles_f16<false>(x >> 8, a.one), nibbles_f16<false>(y >> 8, a.one));
-              product(o[4 * (q + e) + 3], nibbles_f16<true>(x >> 8, a.one), nibbles_f16<true>(y >> 8, a.one));
-            }
+            product(o[4 * (q + e)], nibbles_f16<false>(x, a.one), nibbles_f16<false>(y, a.one));
+            product(o[4 * (q + e) + 1], nibbles_f16<true>(x, a.one), nibbles_f16<true>(y, a.one));
+            product(o[4 * (q + e) + 2], nibbles_f16<false>(x >> 8, a.one), nibbles_f16<false>(y >> 8, a.one));
+            product(o[4 * (q + e) + 3], nibbles_f16<true>(x >> 8, a.one), nibbles_f16<true>(y >> 8, a.one));
           }
         }
       }
-      tile = tile + S::kTileBytes == ring + (warp + 1) * S::kRing ? ring + warp * S::kRing : tile + S::kTileBytes;
+      run = run + S::kRunBytes == ring + (warp + 1) * S::kRing ? ring + warp * S::kRing : run + S::kRunBytes;
     }
     cp_async_wait<0>();
 
@@ -750,9 +755,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) k_attn_join(const __grid_c
   const uint32_t rows = a.c.n_heads * a.head_chunks;
   const uint32_t row = per_head ? blockIdx.x / a.group * a.head_chunks + blockIdx.x % a.group / heads_of_cta : blockIdx.x;
   const uint32_t per_row = units_of(a, __ldg(a.lens + b));
-  uint32_t before = 0, all = 0;  // units of the sequences before b, and of all
+  uint32_t before = 0, all = 0;  // places of the sequences before b, and of all
   for (int i = lane; i < a.batch; i += 32) {
-    const uint32_t n = units_of(a, __ldg(a.lens + i));
+    const uint32_t n = cost_of(a, __ldg(a.lens + i));
     all += n;
     if (i < b) before += n;
   }
@@ -761,7 +766,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) k_attn_join(const __grid_c
   asm volatile("griddepcontrol.wait;" ::: "memory");  // by every thread: this grid ends after k_attn's
   if (per_row <= 1) return;
   const Parts parts(all, min((uint32_t)a.ctas, all));
-  const uint32_t c0 = parts.cta_of(before + row * per_row), c1 = parts.cta_of(before + (row + 1) * per_row - 1);
+  const uint32_t first = before + row * (per_row + kRowCost) + kRowCost;  // the row's first unit
+  const uint32_t c0 = parts.cta_of(first), c1 = parts.cta_of(first + per_row - 1);
   if (c0 == c1) return;  // one CTA had the whole row and has written it
   const int n = (int)(c1 - c0 + 1);
   const int kv = row / a.head_chunks, h0 = kv * a.group + row % a.head_chunks * heads_of_cta;
@@ -853,8 +859,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) k_attn_join(const __grid_c
 
 int heads_of_cta(int group) { return group > 8 ? 16 : 8; }
 
-// CTAs of k_attn: as many as the SMs hold at once (each takes an equal part of all the work), or a unit each.
-int64_t most_units(int64_t batch, int64_t rows, int64_t limit) { return batch * rows * ((limit + kUnit - 1) / kUnit); }
+// CTAs of k_attn: as many as the SMs hold at once (each takes an equal part of the line), or one a place.
+int64_t most_places(int64_t batch, int64_t rows, int64_t limit) { return batch * rows * ((limit + kUnit - 1) / kUnit + kRowCost); }
 bool has_parts(int64_t limit) { return limit > kUnit; }
 
 // What launch_main does: fill in a.ctas only; launch with room for `bytes` of workspace (IMQ_ERR_BUFFER if that is
@@ -883,7 +889,7 @@ imq_status launch_shape(AttnArgs& a, int num_sms, int64_t rows, const Launch& l)
       return IMQ_ERR_CUDA;
     resident[dev].store(per_sm, std::memory_order_release);
   }
-  const int64_t most = most_units(a.batch, rows, a.limit);
+  const int64_t most = most_places(a.batch, rows, a.limit);
   a.ctas = (int)(most < 1 ? 1 : most < (int64_t)per_sm * num_sms ? most : (int64_t)per_sm * num_sms);
   if (l.only_count) return IMQ_OK;
   if (has_parts(a.limit)) {
@@ -921,7 +927,7 @@ imq_status check_shape(const imq_kv_cache* c, int64_t batch, int32_t q_heads, in
   if (s != IMQ_OK) return s;
   if (batch < 0 || q_heads < 1 || max_len < 0 || q_heads % c->n_heads != 0) return IMQ_ERR_ARG;
   const int64_t group = q_heads / c->n_heads, per = heads_of_cta((int)group), rows = (group + per - 1) / per * c->n_heads;
-  if (batch > 65535 || q_heads > 65535 || max_len > (1 << 30) || most_units(batch, rows, max_len) > INT32_MAX)
+  if (batch > 65535 || q_heads > 65535 || max_len > (1 << 30) || most_places(batch, rows, max_len) > INT32_MAX)
     return IMQ_ERR_UNSUPPORTED;
   return IMQ_OK;
 }
