@@ -269,8 +269,8 @@ __global__ void __launch_bounds__(512) k_w4_dequantize_cols(DequantArgs a) {
 //     part with up to 2 tokens, an operand for each part with more.
 //   - The sums of a group are scaled by its step in fp32.
 // A CTA takes 16 kR output channels at a time; its eight warps take the blocks of 128 inputs in turn, each with its own
-// ring of asynchronous copies (every lane copies the 16-byte pieces that it will use itself) that runs on from one
-// set of channels to the next.  The warps' sums meet in shared memory, in a fixed order.
+// ring of asynchronous copies that runs on from one set of channels to the next.  The warps' sums meet in shared
+// memory, in a fixed order.
 struct MatvecArgs {
   const uint8_t* codes;
   int64_t ldc;
@@ -298,9 +298,10 @@ struct MvShape {
   static constexpr bool kPacked = kF32 && kTiles == 1;
   static constexpr int kParts = kF32 ? 3 : 1;
   static constexpr int kTok = kPacked ? 1 : kTiles / kParts;  // tokens of a lane
-  static constexpr int kXPieces = kTok * 4 * (kF32 ? 2 : 1);  // 16-byte pieces of X of a lane and block
+  // X of a stage: a row of 128 entries a token, and a gap so that the eight lanes that read together meet other banks
+  static constexpr int kXRows = kPacked ? 2 : 8 * kTok, kXPitch = kBlock * (int)sizeof(T) + (kF32 ? 16 : 64);
   static constexpr int kPerBlock = kBlock / kGroup;           // steps of a row and block
-  static constexpr int kStepsAt = (2 * kR + kXPieces) * 512;
+  static constexpr int kXAt = 2 * kR * 512, kStepsAt = kXAt + kXRows * kXPitch;
   static constexpr int kStage = kStepsAt + 2 * kR * 8 * kPerBlock * 4;
   static constexpr int kPerSm = kTiles * kR <= 2 ? 2 : 1;     // CTAs an SM, by registers
   static constexpr int kCols = kTiles * 8;
@@ -334,14 +335,12 @@ __global__ void __launch_bounds__(kMvWarps * 32, MvShape<T, kGroup, kTiles, kR>:
 
   // Columns without a token hold what lies in shared memory: a column's sums depend on no other column, and theirs are
   // not stored.
-  const T* xp[S::kTok];  // this lane's first entry
-  bool has[S::kTok];
-#pragma unroll
-  for (int t = 0; t < S::kTok; ++t) {
-    const int tok = S::kPacked ? g / 3 : 8 * t + g;
-    has[t] = tok < tokens;
-    xp[t] = static_cast<const T*>(a.X) + (m0 + (has[t] ? tok : 0)) * a.ldx + 8 * c;
-  }
+  // Copies of X take its rows in order: a row's 128 entries are kRowLanes copies of 16 bytes.
+  constexpr int kRowLanes = kBlock / kPer16, kRowsAtOnce = 32 / kRowLanes;
+  const T* const x16 = static_cast<const T*>(a.X) + (m0 + lane / kRowLanes) * a.ldx + lane % kRowLanes * kPer16;
+  const T* const x0 = static_cast<const T*>(a.X) + m0 * a.ldx;
+  // where this lane's entries lie in a stage
+  const uint32_t x_at = S::kXAt + (S::kPacked ? min(g / 3, 1) : g) * S::kXPitch + 8 * c * (int)sizeof(T);
 
   // the next block to copy: set, its block, ring stage, and where the set's rows lie
   int set_in = blockIdx.x, kb_in = warp, stage_in = 0;
@@ -360,7 +359,7 @@ __global__ void __launch_bounds__(kMvWarps * 32, MvShape<T, kGroup, kTiles, kR>:
   auto issue = [&]() {
     if (set_in < sets && per_set > 0) {
       uint8_t* const to = mine + stage_in * S::kStage;
-      const uint32_t dst = smem_addr(to) + lane * 16, dst4 = smem_addr(to) + S::kStepsAt + (g * kPerBlock + c) * 4;
+      const uint32_t dst = smem_addr(to) + lane * 16, dst_x = smem_addr(to) + S::kXAt, dst4 = smem_addr(to) + S::kStepsAt + (g * kPerBlock + c) * 4;
       const bool steps_on = c < kPerBlock && kb_in * kPerBlock + c < groups;
 #pragma unroll
       for (int r = 0; r < 2 * kR; ++r) {
@@ -368,47 +367,34 @@ __global__ void __launch_bounds__(kMvWarps * 32, MvShape<T, kGroup, kTiles, kR>:
         if (steps_on) cp_async<4>(dst4 + r * 32 * kPerBlock, step_row[r] + kb_in * kPerBlock);
       }
       const int k0 = kb_in * kBlock;
-      constexpr int kPieces = 8 / kPer16;  // of eight entries
       if (a.aligned == 16 && k0 + kBlock <= K) {
 #pragma unroll
-        for (int t = 0; t < S::kTok; ++t)
-          if (has[t]) {
+        for (int q = 0; q < S::kXRows / kRowsAtOnce; ++q)
+          if (q * kRowsAtOnce + lane / kRowLanes < tokens)
+            cp_async<16>(dst_x + q * kRowsAtOnce * S::kXPitch + lane / kRowLanes * S::kXPitch + lane % kRowLanes * 16,
+                         x16 + q * kRowsAtOnce * a.ldx + k0);
+      } else if (a.aligned >= 4) {  // rows that begin anywhere, and their ends: four bytes at a time, zeros behind the end
+        const int left = (K - k0) * (int)sizeof(T);  // bytes of the row
+        const uint8_t* row = reinterpret_cast<const uint8_t*>(x0 + k0);
+        for (int t = 0; t < tokens; ++t, row += a.ldx * (int)sizeof(T)) {
 #pragma unroll
-            for (int h = 0; h < 4; ++h)
-#pragma unroll
-              for (int q = 0; q < kPieces; ++q)
-                cp_async<16>(dst + (2 * kR + (t * 4 + h) * kPieces + q) * 512, xp[t] + k0 + 32 * h + q * kPer16);
+          for (int q = 0; q < kBlock * (int)sizeof(T) / 128; ++q) {
+            const int at = q * 128 + lane * 4, n = min(max(left - at, 0), 4);
+            cp_async_part<4>(dst_x + t * S::kXPitch + at, n ? row + at : a.codes, n);
           }
-      } else if (a.aligned >= 4 && k0 + kBlock <= K) {  // rows that begin anywhere: four bytes at a time
+        }
+      } else {
+        for (int t = 0; t < tokens; t += 2) {  // (loads of two rows under way together)
+          T v[2][4];
 #pragma unroll
-        for (int t = 0; t < S::kTok; ++t)
-          if (has[t]) {
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int h = 0; h < 4; ++h)
+            for (int q = 0; q < 4; ++q)
+              v[j][q] = k0 + 32 * q + lane < K ? x0[min(t + j, tokens - 1) * a.ldx + k0 + 32 * q + lane] : from_f32<T>(0.f);
 #pragma unroll
-              for (int e = 0; e < 2 * (int)sizeof(T); ++e)
-                cp_async<4>(dst + (2 * kR + (t * 4 + h) * kPieces + e / 4) * 512 + e % 4 * 4, xp[t] + k0 + 32 * h + e * (4 / (int)sizeof(T)));
-          }
-      } else {  // the end of a row: four bytes at a time, or an entry
-#pragma unroll 1
-        for (int h = 0; h < 4 * S::kTok; ++h) {
-          const int t = h / 4, k = k0 + 32 * (h % 4);
-          if (!(t ? has[S::kTok - 1] : has[0])) continue;
-          const T* const p = (t ? xp[S::kTok - 1] : xp[0]) + k;
-          const int left = (K - k - 8 * c) * (int)sizeof(T);  // bytes of the row
-          const uint32_t slot = dst + (2 * kR + h * kPieces) * 512;
-          if (a.aligned >= 4) {
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int e = 0; e < 2 * (int)sizeof(T); ++e) {
-              const int n = min(max(left - 4 * e, 0), 4);
-              cp_async_part<4>(slot + e / 4 * 512 + e % 4 * 4, n ? reinterpret_cast<const uint8_t*>(p) + 4 * e : reinterpret_cast<const uint8_t*>(a.codes), n);
-            }
-          } else {
-            T* const at = reinterpret_cast<T*>(to + (2 * kR + h * kPieces) * 512 + lane * 16);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              at[e / kPer16 * (512 / sizeof(T)) + e % kPer16] = e * (int)sizeof(T) < left ? p[e] : from_f32<T>(0.f);
-          }
+            for (int q = 0; q < 4; ++q) reinterpret_cast<T*>(to + S::kXAt + (t + j) * S::kXPitch)[32 * q + lane] = v[j][q];
         }
       }
       stage_in = stage_in + 1 == kStages ? 0 : stage_in + 1;
@@ -427,7 +413,7 @@ __global__ void __launch_bounds__(kMvWarps * 32, MvShape<T, kGroup, kTiles, kR>:
     float total[kR][kTiles][4] = {};
     for (int i = 0; i < per_set; ++i) {
       cp_async_wait<kStages - 2>();
-      __syncwarp();  // the steps were copied by other lanes; every lane is done with the stage that is overwritten now
+      __syncwarp();  // other lanes copied X and the steps; every lane is done with the stage that is overwritten now
       issue();
       const uint8_t* const from = mine + stage * S::kStage;
       stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -445,13 +431,13 @@ __global__ void __launch_bounds__(kMvWarps * 32, MvShape<T, kGroup, kTiles, kR>:
 #pragma unroll
         for (int t = 0; t < S::kTok; ++t) {
           if constexpr (!S::kF32) {
-            const uint4 q = *reinterpret_cast<const uint4*>(from + (2 * kR + t * 4 + h) * 512 + lane * 16);
+            const uint4 q = *reinterpret_cast<const uint4*>(from + x_at + t * 8 * S::kXPitch + h * 64);
             x[t][0] = q.x, x[t][1] = q.y, x[t][2] = q.z, x[t][3] = q.w;
           } else {
             float f[8];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              const float4 y = *reinterpret_cast<const float4*>(from + (2 * kR + (t * 4 + h) * 2 + q) * 512 + lane * 16);
+              const float4 y = *reinterpret_cast<const float4*>(from + x_at + t * 8 * S::kXPitch + h * 128 + q * 16);
               f[4 * q] = y.x, f[4 * q + 1] = y.y, f[4 * q + 2] = y.z, f[4 * q + 3] = y.w;
             }
             if constexpr (S::kPacked) {
