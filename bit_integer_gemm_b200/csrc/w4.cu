@@ -298,8 +298,9 @@ struct MvShape {
   static constexpr bool kPacked = kF32 && kTiles == 1;
   static constexpr int kParts = kF32 ? 3 : 1;
   static constexpr int kTok = kPacked ? 1 : kTiles / kParts;  // tokens of a lane
-  // X of a stage: a row of 128 entries a token, and a gap so that the eight lanes that read together meet other banks
-  static constexpr int kXRows = kPacked ? 2 : 8 * kTok, kXPitch = kBlock * (int)sizeof(T) + (kF32 ? 16 : 64);
+  // X of a stage: a row of 128 entries a token.  In odd rows kSwap bytes change places with the next kSwap (an exclusive
+  // or of the place), so that the eight lanes that read 16 bytes together, from two rows, meet other banks.
+  static constexpr int kXRows = kPacked ? 2 : 8 * kTok, kXPitch = kBlock * (int)sizeof(T), kSwap = kF32 ? 16 : 64;
   static constexpr int kPerBlock = kBlock / kGroup;           // steps of a row and block
   static constexpr int kXAt = 2 * kR * 512, kStepsAt = kXAt + kXRows * kXPitch;
   static constexpr int kStage = kStepsAt + 2 * kR * 8 * kPerBlock * 4;
@@ -333,75 +334,92 @@ __global__ void __launch_bounds__(kMvWarps * 32, MvShape<T, kGroup, kTiles, kR>:
   constexpr int kPerBlock = S::kPerBlock;
   uint8_t* const mine = smem + warp * kStages * S::kStage;
 
-  // Columns without a token hold what lies in shared memory: a column's sums depend on no other column, and theirs are
-  // not stored.
-  // Copies of X take its rows in order: a row's 128 entries are kRowLanes copies of 16 bytes.
+  // Copies of X take its rows in order: a row's 128 entries are kRowLanes copies of 16 bytes.  Columns without a token
+  // hold what lies in shared memory: a column's sums depend on no other column, and theirs are not stored.
   constexpr int kRowLanes = kBlock / kPer16, kRowsAtOnce = 32 / kRowLanes;
-  const T* const x16 = static_cast<const T*>(a.X) + (m0 + lane / kRowLanes) * a.ldx + lane % kRowLanes * kPer16;
-  const T* const x0 = static_cast<const T*>(a.X) + m0 * a.ldx;
+  const int64_t row_bytes = a.ldx * (int)sizeof(T);
+  const uint8_t* const x0 = static_cast<const uint8_t*>(a.X) + m0 * row_bytes;
+  const uint8_t* const x16 = x0 + lane / kRowLanes * row_bytes + lane % kRowLanes * 16;
+  const uint32_t to16 = S::kXAt + lane / kRowLanes * S::kXPitch + (lane % kRowLanes * 16 ^ lane / kRowLanes % 2 * S::kSwap);
+  const int whole = K / kBlock, whole16 = a.aligned == 16 ? whole : 0;  // blocks copied whole, and 16 bytes at a time
   // where this lane's entries lie in a stage
-  const uint32_t x_at = S::kXAt + (S::kPacked ? min(g / 3, 1) : g) * S::kXPitch + 8 * c * (int)sizeof(T);
+  const int x_row = S::kPacked ? min(g / 3, 1) : g, swap = x_row % 2 * S::kSwap;
+  const uint32_t x_at = S::kXAt + x_row * S::kXPitch + (S::kF32 ? 32 * c : 16 * c);
 
   // the next block to copy: set, its block, ring stage, and where the set's rows lie
   int set_in = blockIdx.x, kb_in = warp, stage_in = 0;
+  // The steps of a stage are copied in order too: kStepCopies of them a lane.
+  constexpr int kStepCopies = (16 * kR * kPerBlock + 31) / 32;
   const uint8_t* code_row[2 * kR];
-  const float* step_row[2 * kR];
+  const float* step_row[kStepCopies];
   auto open_set = [&]() {
+    // rows behind the last one read the last one; their sums are not stored
+    const int last = N - 1 - set_in * 16 * kR;
+    const uint8_t* const code0 = a.codes + (int64_t)set_in * (16 * kR) * a.ldc + 16 * c;
+    const float* const step0 = a.steps + (int64_t)set_in * (16 * kR) * a.lds + lane % kPerBlock;
 #pragma unroll
-    for (int r = 0; r < 2 * kR; ++r) {
-      // rows behind the last one read the last one; their sums are not stored
-      const int64_t n = min((int64_t)set_in * 16 * kR + 8 * r + g, (int64_t)N - 1);
-      code_row[r] = a.codes + n * a.ldc + 16 * c;
-      step_row[r] = a.steps + n * a.lds + c;
-    }
+    for (int r = 0; r < 2 * kR; ++r) code_row[r] = code0 + min(8 * r + g, last) * a.ldc;
+#pragma unroll
+    for (int q = 0; q < kStepCopies; ++q) step_row[q] = step0 + min((q * 32 + lane) / kPerBlock, last) * a.lds;
   };
-  open_set();
+  if (set_in < sets) open_set();
   auto issue = [&]() {
     if (set_in < sets && per_set > 0) {
       uint8_t* const to = mine + stage_in * S::kStage;
-      const uint32_t dst = smem_addr(to) + lane * 16, dst_x = smem_addr(to) + S::kXAt, dst4 = smem_addr(to) + S::kStepsAt + (g * kPerBlock + c) * 4;
-      const bool steps_on = c < kPerBlock && kb_in * kPerBlock + c < groups;
+      const uint32_t dst = smem_addr(to), dst_x = dst + S::kXAt;
 #pragma unroll
-      for (int r = 0; r < 2 * kR; ++r) {
-        cp_async<16>(dst + r * 512, code_row[r] + kb_in * kBlockBytes);
-        if (steps_on) cp_async<4>(dst4 + r * 32 * kPerBlock, step_row[r] + kb_in * kPerBlock);
+      for (int r = 0; r < 2 * kR; ++r) cp_async<16>(dst + lane * 16 + r * 512, code_row[r] + (uint32_t)kb_in * kBlockBytes);
+      if (kb_in * kPerBlock + lane % kPerBlock < groups) {
+#pragma unroll
+        for (int q = 0; q < kStepCopies; ++q)
+          if (16 * kR * kPerBlock >= 32 || lane < 16 * kR * kPerBlock)
+            cp_async<4>(dst + S::kStepsAt + (q * 32 + lane) * 4, step_row[q] + (uint32_t)kb_in * kPerBlock);
       }
-      const int k0 = kb_in * kBlock;
-      if (a.aligned == 16 && k0 + kBlock <= K) {
+      const uint32_t k_bytes = (uint32_t)kb_in * (kBlock * (int)sizeof(T));
+      if (kb_in < whole16) {
+        const uint8_t* row = x16 + k_bytes;
 #pragma unroll
-        for (int q = 0; q < S::kXRows / kRowsAtOnce; ++q)
-          if (q * kRowsAtOnce + lane / kRowLanes < tokens)
-            cp_async<16>(dst_x + q * kRowsAtOnce * S::kXPitch + lane / kRowLanes * S::kXPitch + lane % kRowLanes * 16,
-                         x16 + q * kRowsAtOnce * a.ldx + k0);
-      } else if (a.aligned >= 4) {  // rows that begin anywhere, and their ends: four bytes at a time, zeros behind the end
-        const int left = (K - k0) * (int)sizeof(T);  // bytes of the row
-        const uint8_t* row = reinterpret_cast<const uint8_t*>(x0 + k0);
-        for (int t = 0; t < tokens; ++t, row += a.ldx * (int)sizeof(T)) {
+        for (int q = 0; q < S::kXRows / kRowsAtOnce; ++q) {
+          if (q * kRowsAtOnce >= tokens) break;
+          if (kRowsAtOnce == 1 || q * kRowsAtOnce + lane / kRowLanes < tokens) cp_async<16>(dst + (to16 ^ (kRowsAtOnce == 1 ? q % 2 * S::kSwap : 0)) + q * kRowsAtOnce * S::kXPitch, row);
+          row += kRowsAtOnce * row_bytes;
+        }
+      } else if (a.aligned >= 4 && kb_in < whole) {  // rows that begin anywhere: four bytes at a time
+        const uint8_t* row = x0 + k_bytes + lane * 4;
+        uint32_t at = dst_x + lane * 4;
+        for (int t = 0; t < tokens; ++t, row += row_bytes, at += S::kXPitch) {
 #pragma unroll
+          for (int q = 0; q < kBlock * (int)sizeof(T) / 128; ++q) cp_async<4>((at ^ t % 2 * S::kSwap) + q * 128, row + q * 128);
+        }
+      } else if (a.aligned >= 4) {  // the end of a row, zeros behind it
+        const int left = (K - kb_in * kBlock) * (int)sizeof(T);  // bytes
+        for (int t = 0; t < tokens; ++t) {
           for (int q = 0; q < kBlock * (int)sizeof(T) / 128; ++q) {
             const int at = q * 128 + lane * 4, n = min(max(left - at, 0), 4);
-            cp_async_part<4>(dst_x + t * S::kXPitch + at, n ? row + at : a.codes, n);
+            cp_async_part<4>(dst_x + t * S::kXPitch + (at ^ t % 2 * S::kSwap), n ? x0 + t * row_bytes + k_bytes + at : a.codes, n);
           }
         }
       } else {
+        const int k0 = kb_in * kBlock + lane;
         for (int t = 0; t < tokens; t += 2) {  // (loads of two rows under way together)
           T v[2][4];
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              v[j][q] = k0 + 32 * q + lane < K ? x0[min(t + j, tokens - 1) * a.ldx + k0 + 32 * q + lane] : from_f32<T>(0.f);
+              v[j][q] = k0 + 32 * q < K ? *reinterpret_cast<const T*>(x0 + min(t + j, tokens - 1) * row_bytes + (k0 + 32 * q) * (int64_t)sizeof(T))
+                                        : from_f32<T>(0.f);
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) reinterpret_cast<T*>(to + S::kXAt + (t + j) * S::kXPitch)[32 * q + lane] = v[j][q];
+            for (int q = 0; q < 4; ++q) *reinterpret_cast<T*>(to + S::kXAt + (t + j) * S::kXPitch + ((32 * q + lane) * (int)sizeof(T) ^ j * S::kSwap)) = v[j][q];
         }
       }
       stage_in = stage_in + 1 == kStages ? 0 : stage_in + 1;
       kb_in += kMvWarps;
       if (kb_in >= nb) {
         kb_in = warp, set_in += gridDim.x;
-        open_set();
+        if (set_in < sets) open_set();
       }
     }
     cp_async_commit();
@@ -431,13 +449,13 @@ __global__ void __launch_bounds__(kMvWarps * 32, MvShape<T, kGroup, kTiles, kR>:
 #pragma unroll
         for (int t = 0; t < S::kTok; ++t) {
           if constexpr (!S::kF32) {
-            const uint4 q = *reinterpret_cast<const uint4*>(from + x_at + t * 8 * S::kXPitch + h * 64);
+            const uint4 q = *reinterpret_cast<const uint4*>(from + x_at + t * 8 * S::kXPitch + (h * 64 ^ swap));
             x[t][0] = q.x, x[t][1] = q.y, x[t][2] = q.z, x[t][3] = q.w;
           } else {
             float f[8];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              const float4 y = *reinterpret_cast<const float4*>(from + x_at + t * 8 * S::kXPitch + h * 128 + q * 16);
+              const float4 y = *reinterpret_cast<const float4*>(from + x_at + t * 8 * S::kXPitch + h * 128 + (q * 16 ^ swap));
               f[4 * q] = y.x, f[4 * q + 1] = y.y, f[4 * q + 2] = y.z, f[4 * q + 3] = y.w;
             }
             if constexpr (S::kPacked) {
