@@ -554,10 +554,12 @@ imq_status matvec_shape(const MatvecArgs& a, int num_sms, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? IMQ_OK : IMQ_ERR_CUDA;
 }
 
-// Two sets of 16 channels at a time where there are enough of them for every SM: X is read and cut up half as often.
+// 32 channels a CTA where 16 would put a second CTA on some SMs: X is read and cut up half as often, and the SMs have
+// the same work.  Below that 16: twice the CTAs.  bf16, one token, K = 11008: N = 2560 in 8.3 us with 32 and 8.8 with 16,
+// N = 2048 in 8.2 and 6.4; fp32, four tokens: 14.3 and 19.7, 14.2 and 10.6.
 template <typename T, int kGroup, int kTiles>
 imq_status matvec_rows(const MatvecArgs& a, int num_sms, cudaStream_t st) {
-  return a.N > 32 * num_sms ? matvec_shape<T, kGroup, kTiles, 2>(a, num_sms, st) : matvec_shape<T, kGroup, kTiles, 1>(a, num_sms, st);
+  return a.N > 16 * num_sms ? matvec_shape<T, kGroup, kTiles, 2>(a, num_sms, st) : matvec_shape<T, kGroup, kTiles, 1>(a, num_sms, st);
 }
 
 template <typename T, int kGroup>
