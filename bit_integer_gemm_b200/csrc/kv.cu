@@ -20,6 +20,9 @@ struct VecArgs {
   int head_shift, page_shift;  // heads = 2^head_shift, page_size = 2^page_shift, or -1
   int32_t* status;
   uint32_t one;  // kOneF16
+  int64_t slots_of_cache;
+  uint32_t k_stride16, v_stride16, s_stride16;  // of pages, in 16 bytes
+  uint32_t vec16;                               // of a vector, in 16 bytes
 };
 
 // Tokens a lane group takes, their loads under way together: four where that still fills the SMs twice (8191 tokens of 8
@@ -27,23 +30,24 @@ struct VecArgs {
 // back: 7.2 us with four, 4.7 with two).
 constexpr int kManyTokens = 4;
 
-// The cache place of a token's vector: page, and vector within the page's head block.  False for a token that is skipped.
-__device__ __forceinline__ bool locate(const VecArgs& a, int64_t tok, int head, bool report, uint32_t* page, int64_t* at) {
-  const int64_t slot = tok < a.n ? a.slots[tok] : -1;
+// Where a token's vectors of a head lie: in the keys and the values, and their page in the steps, in 16 bytes (every
+// offset of a legal cache fits); and which vector of its page it is.
+struct Place {
+  uint32_t k, v, s_page, vec;
+};
+__device__ __forceinline__ float2* steps_at(const imq_kv_cache& c, const Place& at) {
+  return reinterpret_cast<float2*>(c.steps + (uint64_t)at.s_page * 4) + at.vec;
+}
+// False for a token that is skipped.  A legal cache has fewer than 2^32 slots.
+__device__ __forceinline__ bool locate(const VecArgs& a, int64_t slot, int head, bool report, Place* at) {
   if (slot < 0) return false;
-  if (slot >= a.c.n_pages * a.c.page_size) {
+  if (slot >= a.slots_of_cache) {
     if (report) set_status(a.status, IMQ_ERR_BOUNDS);
     return false;
   }
-  uint32_t p, place;
-  if (slot <= UINT32_MAX) {
-    p = a.page_shift >= 0 ? (uint32_t)slot >> a.page_shift : (uint32_t)slot / (uint32_t)a.c.page_size;
-    place = (uint32_t)slot - p * (uint32_t)a.c.page_size;
-  } else {
-    p = (uint32_t)(slot / a.c.page_size), place = (uint32_t)(slot % a.c.page_size);
-  }
-  *page = p;
-  *at = head * (int64_t)a.c.page_size + place;
+  const uint32_t x = (uint32_t)slot, size = a.c.page_size;
+  const uint32_t p = a.page_shift >= 0 ? x >> a.page_shift : x / size, vec = head * size + (x - p * size);
+  *at = {p * a.k_stride16 + vec * a.vec16, p * a.v_stride16 + vec * a.vec16, p * a.s_stride16, vec};
   return true;
 }
 
@@ -112,7 +116,7 @@ __device__ __forceinline__ void store_vec(float* p, bool vec, const float (&x)[4
 template <typename T, int kBits, int kLanes, int kTokens>
 __global__ void __launch_bounds__(256) k_kv_write(const __grid_constant__ VecArgs a) {
   const imq_kv_cache& c = a.c;
-  const int i = threadIdx.x % kLanes, vec_bytes = c.head_dim * kBits / 8;
+  const int i = threadIdx.x % kLanes;
   const uint32_t unit = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
   const uint32_t set = a.head_shift >= 0 ? unit >> a.head_shift : unit / (uint32_t)c.n_heads;
   const int64_t tok0 = (int64_t)set * kTokens;
@@ -126,11 +130,9 @@ __global__ void __launch_bounds__(256) k_kv_write(const __grid_constant__ VecArg
     if (lane && tok0 + j < a.n) k[j].load(kp0 + j * a.k_tok, a.aligned), v[j].load(vp0 + j * a.v_tok, a.aligned);
     else k[j].clear(), v[j].clear();
   }
-  uint32_t page[kTokens];
-  int64_t at[kTokens];
-  bool on[kTokens];
+  int64_t slot[kTokens];
 #pragma unroll
-  for (int j = 0; j < kTokens; ++j) on[j] = locate(a, tok0 + j, head, i == 0, &page[j], &at[j]);
+  for (int j = 0; j < kTokens; ++j) slot[j] = tok0 + j < a.n ? a.slots[tok0 + j] : -1;
   uint32_t key[2][kTokens];
 #pragma unroll
   for (int j = 0; j < kTokens; ++j) key[0][j] = k[j].key(), key[1][j] = v[j].key();
@@ -150,9 +152,10 @@ __global__ void __launch_bounds__(256) k_kv_write(const __grid_constant__ VecArg
   }
 #pragma unroll
   for (int j = 0; j < kTokens; ++j) {
-    if (!lane || !on[j]) continue;
-    uint8_t* kp = c.k + page[j] * c.k_page_stride + at[j] * vec_bytes + kBits * i;  // eight codes are kBits bytes
-    uint8_t* vp = c.v + page[j] * c.v_page_stride + at[j] * vec_bytes + kBits * i;
+    Place at;
+    if (!locate(a, slot[j], head, i == 0, &at) || !lane) continue;
+    uint8_t* const kp = c.k + (uint64_t)at.k * 16 + kBits * i;  // eight codes are kBits bytes
+    uint8_t* const vp = c.v + (uint64_t)at.v * 16 + kBits * i;
     float x[8];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
@@ -165,7 +168,7 @@ __global__ void __launch_bounds__(256) k_kv_write(const __grid_constant__ VecArg
         *reinterpret_cast<uint2*>(q ? vp : kp) = make_uint2(pack8(x[0], x[1], x[2], x[3], s[q][j]), pack8(x[4], x[5], x[6], x[7], s[q][j]));
     }
     if (i == 0) {
-      *reinterpret_cast<float2*>(c.steps + page[j] * c.steps_page_stride + at[j] * 2) = make_float2(step[0][j], step[1][j]);
+      *steps_at(c, at) = make_float2(step[0][j], step[1][j]);
       if (!key_finite(key[0][j]) || !key_finite(key[1][j])) set_status(a.status, IMQ_ERR_NONFINITE);
     }
   }
@@ -177,7 +180,7 @@ template <typename T, int kBits, int kLanes, int kTokens>
 __global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ VecArgs a) {
   constexpr int kMine = 16 / sizeof(T), kWords = kMine * kBits > 32 ? 2 : 1;
   const imq_kv_cache& c = a.c;
-  const int i = threadIdx.x % kLanes, vec_bytes = c.head_dim * kBits / 8;
+  const int i = threadIdx.x % kLanes;
   const uint32_t unit = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
   const uint32_t set = a.head_shift >= 0 ? unit >> a.head_shift : unit / (uint32_t)c.n_heads;
   const int64_t tok0 = (int64_t)set * kTokens;
@@ -187,15 +190,17 @@ __global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ VecArgs
   uint32_t kw[kTokens][kWords], vw[kTokens][kWords];
   float2 step[kTokens];
   bool on[kTokens];
+  int64_t slot[kTokens];
+#pragma unroll
+  for (int j = 0; j < kTokens; ++j) slot[j] = tok0 + j < a.n ? a.slots[tok0 + j] : -1;
 #pragma unroll
   for (int j = 0; j < kTokens; ++j) {
-    uint32_t page;
-    int64_t at;
-    on[j] = locate(a, tok0 + j, head, i == 0, &page, &at) && kMine * i < c.head_dim;
+    Place at;
+    on[j] = locate(a, slot[j], head, i == 0, &at) && kMine * i < c.head_dim;
     if (!on[j]) continue;
-    const uint8_t* kp = c.k + page * c.k_page_stride + at * vec_bytes + from;
-    const uint8_t* vp = c.v + page * c.v_page_stride + at * vec_bytes + from;
-    step[j] = *reinterpret_cast<const float2*>(c.steps + page * c.steps_page_stride + at * 2);
+    const uint8_t* const kp = c.k + (uint64_t)at.k * 16 + from;
+    const uint8_t* const vp = c.v + (uint64_t)at.v * 16 + from;
+    step[j] = *steps_at(c, at);
     if constexpr (kWords == 2) {
       const uint2 x = *reinterpret_cast<const uint2*>(kp), y = *reinterpret_cast<const uint2*>(vp);
       kw[j][0] = x.x, kw[j][1] = x.y, vw[j][0] = y.x, vw[j][1] = y.y;
@@ -271,7 +276,9 @@ imq_status launch(bool write, const imq_kv_cache* cache, void* K, int64_t k_tok,
   if (s != IMQ_OK) return s;
   const int64_t strides = ((K ? k_tok | k_head : 0) | (V ? v_tok | v_head : 0)) * size;
   VecArgs a{*cache, K, V, n, k_tok, k_head, v_tok, v_head, slots, ((kp | vp | (uintptr_t)strides) & 15) == 0,
-            log2_or(cache->n_heads), log2_or(cache->page_size), ds->status, kOneF16};
+            log2_or(cache->n_heads), log2_or(cache->page_size), ds->status, kOneF16,
+            cache->n_pages * cache->page_size, (uint32_t)(cache->k_page_stride / 16), (uint32_t)(cache->v_page_stride / 16),
+            (uint32_t)(cache->steps_page_stride / 4), (uint32_t)(cache->head_dim * cache->bits / 128)};
   if (t == IMQ_F32) {
     if (cache->bits == 4) run<float, 4>(write, a, ds->num_sms, st);
     else run<float, 8>(write, a, ds->num_sms, st);

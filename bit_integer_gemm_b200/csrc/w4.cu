@@ -41,12 +41,9 @@ __device__ __forceinline__ uint32_t max_key(const float (&x)[8]) {
 // Row kernels (W stored N x K): a warp takes 256 inputs (two blocks) of four rows, 8 inputs of each a lane.
 constexpr int kRows = 4;
 
-// Eight consecutive entries for each lane of the warp, from 256 consecutive ones of a row that begin anywhere: read in
-// order, turned in shared memory (`turn`, 288 floats of the warp's own, a float of padding every 8 entries).
-template <typename T>
-__device__ __forceinline__ void load256(const T* p, int left, float* turn, int lane, float (&x)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = e * 32 + lane < left ? to_f32(p[e * 32 + lane]) : 0.f;
+// x[e] = entry e * 32 + lane of 256 consecutive ones, becomes entry 8 * lane + e: turned in shared memory (`turn`, 288
+// floats of the warp's own, a float of padding every 8 entries).
+__device__ __forceinline__ void turn256(float* turn, int lane, float (&x)[8]) {
   __syncwarp();
 #pragma unroll
   for (int e = 0; e < 8; ++e) turn[e * 36 + lane + lane / 8] = x[e];
@@ -68,9 +65,15 @@ __global__ void __launch_bounds__(256) k_w4_quantize_rows(QuantArgs a) {
   if (a.vec && k0 + 256 <= K) {
 #pragma unroll
     for (int j = 0; j < kRows; ++j) load8(p + (n0 + j < N ? j : 0) * a.ldw + 8 * lane, x[j]);
-  } else {
+  } else {  // rows that begin anywhere, and their ends: read in order, all of them before the first is turned
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) load256(p + (n0 + j < N ? j : 0) * a.ldw, K - k0, s_turn[warp], lane, x[j]);
+    for (int j = 0; j < kRows; ++j) {
+      const T* const row = p + (n0 + j < N ? j : 0) * a.ldw + lane;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[j][e] = k0 + e * 32 + lane < K ? to_f32(row[e * 32]) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) turn256(s_turn[warp], lane, x[j]);
   }
   uint32_t key[kRows];
 #pragma unroll
@@ -95,59 +98,97 @@ __global__ void __launch_bounds__(256) k_w4_quantize_rows(QuantArgs a) {
   }
 }
 
-// Column kernels (W stored K x N): a CTA takes 128 inputs of 64 channels.  Warp w holds the inputs 8w .. 8w + 7, a lane
-// two channels: what it reads in order is what it packs; only the groups' scales and the packed words cross warps.
+// Column kernels (W stored K x N): a CTA takes 128 inputs of 64 channels, a warp 32 of the inputs, a lane two channels:
+// what it reads in order, 32 loads under way together, is four of its words a channel.  Only the words, and of groups
+// above 32 the largest entries, pass through shared memory.
 constexpr int kColChannels = 64;
+// Two channels' entries of 32 inputs as they lie in memory.
 template <typename T>
-__global__ void __launch_bounds__(512) k_w4_quantize_cols(QuantArgs a) {
-  __shared__ uint32_t s_key[16][kColChannels], s_word[kColChannels][17];
-  __shared__ float s_scale[4][kColChannels];
-  const int k0 = blockIdx.y * kBlock, n0 = blockIdx.x * kColChannels, K = (int)a.K, N = (int)a.N;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = k0 + 8 * warp, n = n0 + 2 * lane;
-  const T* const p = static_cast<const T*>(a.W) + k * a.ldw + n;
-  float x[2][8];
-  if (a.vec && k + 8 <= K && n + 1 < N) {
+struct Column;
+template <>
+struct Column<__nv_bfloat16> {
+  uint32_t w[32];
+  __device__ __forceinline__ void load(int e, const __nv_bfloat16* p) { w[e] = __ldcs(reinterpret_cast<const uint32_t*>(p)); }
+  __device__ __forceinline__ void load(int e, const __nv_bfloat16* p, bool first, bool second) {
+    w[e] = (first ? (uint32_t)__bfloat16_as_ushort(p[0]) : 0u) | (second ? (uint32_t)__bfloat16_as_ushort(p[1]) << 16 : 0u);
+  }
+  __device__ __forceinline__ float entry(int e, int channel) const { return __uint_as_float(channel ? w[e] & 0xFFFF0000u : w[e] << 16); }
+  // abs_key of each channel's largest entry, both at a time
+  __device__ __forceinline__ uint2 key() const {
+    uint32_t m = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if constexpr (sizeof(T) == 4) {
-        const float2 v = *reinterpret_cast<const float2*>(p + e * a.ldw);
-        x[0][e] = v.x, x[1][e] = v.y;
-      } else {
-        const uint32_t v = *reinterpret_cast<const uint32_t*>(p + e * a.ldw);
-        x[0][e] = __uint_as_float(v << 16), x[1][e] = __uint_as_float(v & 0xFFFF0000u);
-      }
-    }
+    for (int e = 0; e < 32; ++e) m = __vmaxu2(m, w[e] & 0x7FFF7FFFu);
+    return make_uint2(m << 16, m & 0xFFFF0000u);
+  }
+};
+template <>
+struct Column<float> {
+  float2 w[32];
+  __device__ __forceinline__ void load(int e, const float* p) { w[e] = __ldcs(reinterpret_cast<const float2*>(p)); }
+  __device__ __forceinline__ void load(int e, const float* p, bool first, bool second) {
+    w[e] = make_float2(first ? p[0] : 0.f, second ? p[1] : 0.f);
+  }
+  __device__ __forceinline__ float entry(int e, int channel) const { return channel ? w[e].y : w[e].x; }
+  __device__ __forceinline__ uint2 key() const {
+    uint2 m = make_uint2(0u, 0u);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) m.x = max(m.x, abs_key(w[e].x)), m.y = max(m.y, abs_key(w[e].y));
+    return m;
+  }
+};
+// Where word i of a channel of the CTA lies in shared memory.
+__device__ __forceinline__ int col_word(int channel, int i) { return (channel % 2 * 32 + channel / 2) * 17 + i; }
+
+template <typename T>
+__global__ void __launch_bounds__(128) k_w4_quantize_cols(QuantArgs a) {
+  __shared__ uint2 s_key[4][32];
+  __shared__ uint32_t s_word[kColChannels * 17];
+  const int k0 = blockIdx.y * kBlock, n0 = blockIdx.x * kColChannels, K = (int)a.K, N = (int)a.N;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = k0 + 32 * warp, n = n0 + 2 * lane;
+  const T* const p = static_cast<const T*>(a.W) + k * a.ldw + n;
+  Column<T> x;
+  if (a.vec && k + 32 <= K && n + 1 < N) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) x.load(e, p + e * a.ldw);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[0][e] = k + e < K && n < N ? to_f32(p[e * a.ldw]) : 0.f;
-      x[1][e] = k + e < K && n + 1 < N ? to_f32(p[e * a.ldw + 1]) : 0.f;
-    }
+    for (int e = 0; e < 32; ++e) x.load(e, p + e * a.ldw, k + e < K && n < N, k + e < K && n + 1 < N);
   }
-  *reinterpret_cast<uint2*>(&s_key[warp][2 * lane]) = make_uint2(max_key(x[0]), max_key(x[1]));
-  __syncthreads();
-  const int log8 = a.log_group - 3;  // a group is 2^log8 warps
-  if (threadIdx.x < kColChannels << (4 - log8)) {
-    const int c = threadIdx.x % kColChannels, group = threadIdx.x / kColChannels, at = k0 + (group << a.log_group);
-    uint32_t key = 0;
-    for (int o = 0; o < 1 << log8; ++o) key = max(key, s_key[(group << log8) + o][c]);
-    float s, step;
-    group_scale(key, 7.f, &s, &step);
-    s_scale[group][c] = s;
-    if (n0 + c < N && at < K) {
-      a.steps[(n0 + c) * a.lds + (at >> a.log_group)] = step;
-      if (!key_finite(key)) set_status(a.status, IMQ_ERR_NONFINITE);
-    }
+  uint2 key = x.key();
+  const int warps = 1 << (a.log_group - 5);  // of a group
+  if (warps > 1) {
+    s_key[warp][lane] = key;
+    __syncthreads();
+    const int first = warp & ~(warps - 1);
+    for (int w = first; w < first + warps; ++w) key.x = max(key.x, s_key[w][lane].x), key.y = max(key.y, s_key[w][lane].y);
   }
+  float s[2], step[2];
+  group_scale(key.x, 7.f, &s[0], &step[0]);
+  group_scale(key.y, 7.f, &s[1], &step[1]);
+  if ((warp & (warps - 1)) == 0 && k < K) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (n + j < N) {
+        a.steps[(n + j) * a.lds + (k >> a.log_group)] = step[j];
+        if (!key_finite(j ? key.y : key.x)) set_status(a.status, IMQ_ERR_NONFINITE);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = x.entry(8 * i + e, j);
+      s_word[col_word(2 * lane + j, 4 * i + warp)] = pack4(y, s[j]);
+    }
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < 2; ++j) s_word[2 * lane + j][word_of(warp)] = pack4(x[j], s_scale[warp >> log8][2 * lane + j]);
-  __syncthreads();
-#pragma unroll
-  for (int q = 0; q < kColChannels * 16 / 512; ++q) {
-    const int c = threadIdx.x / 16 + 32 * q;
+  for (int q = 0; q < 2; ++q) {
+    const int c = threadIdx.x / 4 + 32 * q, i = threadIdx.x % 4 * 4;
+    const uint32_t* const w = s_word + col_word(c, i);
     if (n0 + c < N)
-      reinterpret_cast<uint32_t*>(a.codes + (n0 + c) * a.ldc + (int64_t)blockIdx.y * kBlockBytes)[threadIdx.x % 16] = s_word[c][threadIdx.x % 16];
+      *reinterpret_cast<uint4*>(a.codes + (n0 + c) * a.ldc + (int64_t)blockIdx.y * kBlockBytes + 4 * i) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -222,38 +263,45 @@ __global__ void __launch_bounds__(256) k_w4_dequantize_rows(DequantArgs a) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(512) k_w4_dequantize_cols(DequantArgs a) {
-  __shared__ uint32_t s_word[kColChannels][17];
-  __shared__ float s_step[4][kColChannels];
+__global__ void __launch_bounds__(128) k_w4_dequantize_cols(DequantArgs a) {
+  __shared__ uint32_t s_word[kColChannels * 17];
   const int k0 = blockIdx.y * kBlock, n0 = blockIdx.x * kColChannels, K = (int)a.K, N = (int)a.N;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = k0 + 8 * warp, n = n0 + 2 * lane;
-  const int log8 = a.log_group - 3;  // a group is 2^log8 warps
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = k0 + 32 * warp, n = n0 + 2 * lane;
+  uint4 w[2];
 #pragma unroll
-  for (int q = 0; q < kColChannels * 16 / 512; ++q) {
-    const int c = threadIdx.x / 16 + 32 * q;
-    s_word[c][threadIdx.x % 16] =
-        n0 + c < N ? reinterpret_cast<const uint32_t*>(a.codes + (n0 + c) * a.ldc + (int64_t)blockIdx.y * kBlockBytes)[threadIdx.x % 16] : 0u;
+  for (int q = 0; q < 2; ++q) {
+    const int c = min(threadIdx.x / 4 + 32 * q, N - 1 - n0);  // (channels behind the last one: not stored)
+    w[q] = *reinterpret_cast<const uint4*>(a.codes + (n0 + c) * a.ldc + (int64_t)blockIdx.y * kBlockBytes + threadIdx.x % 4 * 16);
   }
-  if (threadIdx.x < kColChannels << (4 - log8)) {
-    const int c = threadIdx.x % kColChannels, group = threadIdx.x / kColChannels, at = k0 + (group << a.log_group);
-    s_step[group][c] = n0 + c < N && at < K ? a.steps[(n0 + c) * a.lds + (at >> a.log_group)] : 0.f;
+  float step[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) step[j] = n + j < N && k < K ? a.steps[(n + j) * a.lds + (k >> a.log_group)] : 0.f;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    uint32_t* const to = s_word + col_word(threadIdx.x / 4 + 32 * q, threadIdx.x % 4 * 4);
+    to[0] = w[q].x, to[1] = w[q].y, to[2] = w[q].z, to[3] = w[q].w;
   }
   __syncthreads();
-  float x[2][8];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) word_values(s_word[2 * lane + j][word_of(warp)], s_step[warp >> log8][2 * lane + j], a.one, x[j]);
   T* const out = static_cast<T*>(a.W) + k * a.ldw + n;
-  if (a.vec && k + 8 <= K && n + 1 < N) {
+  const bool whole = a.vec && k + 32 <= K && n + 1 < N;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if constexpr (sizeof(T) == 4) *reinterpret_cast<float2*>(out + e * a.ldw) = make_float2(x[0][e], x[1][e]);
-      else *reinterpret_cast<uint32_t*>(out + e * a.ldw) = bf16_pair(x[0][e], x[1][e]);
-    }
-  } else {
+  for (int i = 0; i < 4; ++i) {
+    float x[2][8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (k + e < K && n < N) out[e * a.ldw] = from_f32<T>(x[0][e]);
-      if (k + e < K && n + 1 < N) out[e * a.ldw + 1] = from_f32<T>(x[1][e]);
+    for (int j = 0; j < 2; ++j) word_values(s_word[col_word(2 * lane + j, 4 * i + warp)], step[j], a.one, x[j]);
+    T* const to = out + 8 * i * a.ldw;
+    if (whole) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if constexpr (sizeof(T) == 4) *reinterpret_cast<float2*>(to + e * a.ldw) = make_float2(x[0][e], x[1][e]);
+        else *reinterpret_cast<uint32_t*>(to + e * a.ldw) = bf16_pair(x[0][e], x[1][e]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (k + 8 * i + e < K && n < N) to[e * a.ldw] = from_f32<T>(x[0][e]);
+        if (k + 8 * i + e < K && n + 1 < N) to[e * a.ldw + 1] = from_f32<T>(x[1][e]);
+      }
     }
   }
 }
@@ -633,9 +681,9 @@ imq_status launch_w4_quantize(const void* W, imq_dtype wt, int64_t K, int64_t N,
     if (nb > 65535) return IMQ_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)((N + kColChannels - 1) / kColChannels), (unsigned)nb);
     if (wt == IMQ_F32)
-      k_w4_quantize_cols<float><<<grid, 512, 0, st>>>(a);
+      k_w4_quantize_cols<float><<<grid, 128, 0, st>>>(a);
     else
-      k_w4_quantize_cols<__nv_bfloat16><<<grid, 512, 0, st>>>(a);
+      k_w4_quantize_cols<__nv_bfloat16><<<grid, 128, 0, st>>>(a);
   }
   return launched();
 }
@@ -660,9 +708,9 @@ imq_status launch_w4_dequantize(const uint8_t* codes, int64_t ldc, const float* 
     if (nb > 65535) return IMQ_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)((N + kColChannels - 1) / kColChannels), (unsigned)nb);
     if (wt == IMQ_F32)
-      k_w4_dequantize_cols<float><<<grid, 512, 0, st>>>(a);
+      k_w4_dequantize_cols<float><<<grid, 128, 0, st>>>(a);
     else
-      k_w4_dequantize_cols<__nv_bfloat16><<<grid, 512, 0, st>>>(a);
+      k_w4_dequantize_cols<__nv_bfloat16><<<grid, 128, 0, st>>>(a);
   }
   return launched();
 }
