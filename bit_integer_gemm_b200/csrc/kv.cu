@@ -4,6 +4,8 @@
 // A vector (one head's key or value of one token) is one quantisation group.  D / 8 lanes take a vector, 8
 // entries each: the largest |x| by shuffles, the codes packed to one word (4 bits) or two (8 bits) a lane.
 // A lane group does a token's key and value of a head together, so their two steps are one 8-byte store.
+#include <type_traits>
+
 #include "lowbit.cuh"
 #include "internal.h"
 
@@ -57,8 +59,9 @@ struct Raw {
   static constexpr int kWords = 2 * sizeof(T);
   uint32_t w[kWords];
 
-  __device__ __forceinline__ void load(const T* p, bool vec) {
-    if (vec) {
+  template <bool kVec>
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (kVec) {
 #pragma unroll
       for (int q = 0; q < kWords / 4; ++q) {
         const uint4 v = reinterpret_cast<const uint4*>(p)[q];
@@ -95,16 +98,18 @@ struct Raw {
   }
 };
 // 16 bytes.
-__device__ __forceinline__ void store_vec(__nv_bfloat16* p, bool vec, const float (&x)[8]) {
-  if (vec) {
+template <bool kVec>
+__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&x)[8]) {
+  if constexpr (kVec) {
     store8(p, x);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) p[e] = from_f32<__nv_bfloat16>(x[e]);
   }
 }
-__device__ __forceinline__ void store_vec(float* p, bool vec, const float (&x)[4]) {
-  if (vec) {
+template <bool kVec>
+__device__ __forceinline__ void store_vec(float* p, const float (&x)[4]) {
+  if constexpr (kVec) {
     *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
   } else {
 #pragma unroll
@@ -114,7 +119,7 @@ __device__ __forceinline__ void store_vec(float* p, bool vec, const float (&x)[4
 
 // kLanes: lanes of a vector's group (a power of two >= D / 8; the lanes at and above D / 8 hold zeros).
 template <typename T, int kBits, int kLanes, int kTokens>
-__global__ void __launch_bounds__(256) k_kv_write(const __grid_constant__ VecArgs a) {
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) k_kv_write(const __grid_constant__ VecArgs a) {
   const imq_kv_cache& c = a.c;
   const int i = threadIdx.x % kLanes;
   const uint32_t unit = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
@@ -125,11 +130,15 @@ __global__ void __launch_bounds__(256) k_kv_write(const __grid_constant__ VecArg
   Raw<T> k[kTokens], v[kTokens];
   const T* const kp0 = static_cast<const T*>(a.K) + tok0 * a.k_tok + head * a.k_head + 8 * i;
   const T* const vp0 = static_cast<const T*>(a.V) + tok0 * a.v_tok + head * a.v_head + 8 * i;
+  auto load = [&](auto vec) {
 #pragma unroll
-  for (int j = 0; j < kTokens; ++j) {
-    if (lane && tok0 + j < a.n) k[j].load(kp0 + j * a.k_tok, a.aligned), v[j].load(vp0 + j * a.v_tok, a.aligned);
-    else k[j].clear(), v[j].clear();
-  }
+    for (int j = 0; j < kTokens; ++j) {
+      k[j].clear(), v[j].clear();
+      if (lane && tok0 + j < a.n) k[j].template load<vec>(kp0 + j * a.k_tok), v[j].template load<vec>(vp0 + j * a.v_tok);
+    }
+  };
+  if (a.aligned) load(std::true_type{});
+  else load(std::false_type{});
   int64_t slot[kTokens];
 #pragma unroll
   for (int j = 0; j < kTokens; ++j) slot[j] = tok0 + j < a.n ? a.slots[tok0 + j] : -1;
@@ -218,19 +227,23 @@ __global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ VecArgs
       x[2 * q] = __fmul_rn(v.x, s), x[2 * q + 1] = __fmul_rn(v.y, s);
     }
   };
+  auto write = [&](auto vec) {
 #pragma unroll
-  for (int j = 0; j < kTokens; ++j) {
-    if (!on[j]) continue;
-    float x[kMine];
-    if (a.K) {
-      values(kw[j], step[j].x, x);
-      store_vec(static_cast<T*>(a.K) + (tok0 + j) * a.k_tok + head * a.k_head + kMine * i, a.aligned, x);
+    for (int j = 0; j < kTokens; ++j) {
+      if (!on[j]) continue;
+      float x[kMine];
+      if (a.K) {
+        values(kw[j], step[j].x, x);
+        store_vec<vec>(static_cast<T*>(a.K) + (tok0 + j) * a.k_tok + head * a.k_head + kMine * i, x);
+      }
+      if (a.V) {
+        values(vw[j], step[j].y, x);
+        store_vec<vec>(static_cast<T*>(a.V) + (tok0 + j) * a.v_tok + head * a.v_head + kMine * i, x);
+      }
     }
-    if (a.V) {
-      values(vw[j], step[j].y, x);
-      store_vec(static_cast<T*>(a.V) + (tok0 + j) * a.v_tok + head * a.v_head + kMine * i, a.aligned, x);
-    }
-  }
+  };
+  if (a.aligned) write(std::true_type{});
+  else write(std::false_type{});
 }
 
 int log2_or(int32_t n) { return (n & (n - 1)) == 0 ? __builtin_ctz(n) : -1; }
