@@ -31,9 +31,15 @@
 // head) counts four units more than it has, for its queries and its end: without them a CTA whose part is made of many
 // short rows came last (64 sequences of 1 to 4097 tokens, 8 key heads of 64: 47.2 us, with them 32.6; 16 of up to 8192
 // at 4 bits: 37.0 and 29.0; 2 or 6 to 12 instead of four: 32.6 to 36.2 and 29.4 to 31.0).  A CTA's four warps take runs
-// of 16 tokens in turn, each with its own ring of asynchronous copies (so that a run waits for no barrier but
-// the warp's), and join in shared memory.  Rows that several CTAs
-// share join in k_attn_join from partial sums in the workspace, in a fixed order.
+// of 16 tokens in turn, each with its own ring of asynchronous copies (so that a run waits for no barrier but the
+// warp's), and join in shared memory.  Rows that several CTAs share join in k_attn_join from partial sums in the
+// workspace, in a fixed order.
+//
+// Measured, both kernels: 64 sequences of 2048 tokens, 32 key heads of 128 at 8 bits, 178 us (6.2 TB/s); one of 131072, 8
+// heads, 52 us (5.3 TB/s: memory, and about 8 us of start, ends and join); 64 of 8192 at 4 bits 154 us (3.7 TB/s: a code
+// takes as many instructions as at 8 bits, 345 for 16 tokens and 128 entries, and half the bytes); head size 64 at 8
+// query heads a key head 57 us for 64 of 4096 (5.0 TB/s), size 256 99 us for 64 of 2048 (5.5 TB/s); one sequence of 2048
+// tokens and 32 heads 10.1 us, which is two dependent launches and a CTA's chain of dependent loads.
 #include <atomic>
 #include <type_traits>
 
@@ -745,8 +751,10 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
 
 constexpr int kJoinWarps = 8;
 
-// Joins the parts of a row that several CTAs hold.  Few parts: a warp takes a head; many: all warps share a head's
-// parts.  A lane has four entries (and four more at 128).  A CTA takes a row, or a head where the rows are few.
+// Joins the parts of a row that several CTAs hold.  A lane has four entries (and four more at 128).  Few parts: a warp
+// takes a head; many: all warps share a head's parts (always: 41.6 us for 64 sequences of 1 to 4097 tokens, 32.6 as it
+// is).  A CTA takes a row; a head where that makes no more CTAs than two to one of k_attn's (one sequence of 131072: 52.6
+// us, by rows 58.9; the 64 sequences by heads: 45.2 us).
 __global__ void __launch_bounds__(kJoinWarps * 32, 4) k_attn_join(const __grid_constant__ AttnArgs a, int heads_of_cta, int per_head) {
   __shared__ float s_num[kJoinWarps][256], s_den[kJoinWarps], s_top[kJoinWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.y;

@@ -38,7 +38,9 @@ __device__ __forceinline__ uint32_t max_key(const float (&x)[8]) {
   return key;
 }
 
-// Row kernels (W stored N x K): a warp takes 256 inputs (two blocks) of four rows, 8 inputs of each a lane.
+// Row kernels (W stored N x K): a warp takes 256 inputs (two blocks) of four rows, 8 inputs of each a lane.  Bound: memory
+// for fp32 (11003 x 4097 in 37.9 us, 5.4 TB/s, and back in 34.1), the quantiser's instructions for bf16 (4096 x 4096 in
+// 12.5 us, 3.4 TB/s; back 9.1).
 constexpr int kRows = 4;
 
 // x[e] = entry e * 32 + lane of 256 consecutive ones, becomes entry 8 * lane + e: turned in shared memory (`turn`, 288
@@ -100,7 +102,9 @@ __global__ void __launch_bounds__(256) k_w4_quantize_rows(QuantArgs a) {
 
 // Column kernels (W stored K x N): a CTA takes 128 inputs of 64 channels, a warp 32 of the inputs, a lane two channels:
 // what it reads in order, 32 loads under way together, is four of its words a channel.  Only the words, and of groups
-// above 32 the largest entries, pass through shared memory.
+// above 32 the largest entries, pass through shared memory.  Bound: memory; 4096 x 4096 bf16 in 9.2 us (4.6 TB/s) and
+// back in 9.4, 11008 x 4096 fp32 in 34.9 (5.9) and 35.7.  (A quarter of the inputs a lane, in four times the warps,
+// had too few bytes under way: 13.7 and 12.4 us for the first.)
 constexpr int kColChannels = 64;
 // Two channels' entries of 32 inputs as they lie in memory.
 template <typename T>
@@ -188,7 +192,8 @@ __global__ void __launch_bounds__(128) k_w4_quantize_cols(QuantArgs a) {
     const int c = threadIdx.x / 4 + 32 * q, i = threadIdx.x % 4 * 4;
     const uint32_t* const w = s_word + col_word(c, i);
     if (n0 + c < N)
-      *reinterpret_cast<uint4*>(a.codes + (n0 + c) * a.ldc + (int64_t)blockIdx.y * kBlockBytes + 4 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(a.codes + (n0 + c) * a.ldc + (int64_t)blockIdx.y * kBlockBytes + 4 * i) =
+          make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -309,16 +314,18 @@ __global__ void __launch_bounds__(128) k_w4_dequantize_cols(DequantArgs a) {
 // ------------------------------------------------------------------------------------------------
 // Y = X * W for a few tokens
 // ------------------------------------------------------------------------------------------------
-// Bound: the weight is read once, N K / 2 bytes and the steps, for 2 M N K operations -- memory, as long as turning
-// codes into operands keeps up: eleven instructions for eight codes.  So the product runs on the warp-level tensor
-// core instruction with the weight as the 16-row operand: a conversion serves 8 tokens at once.
+// The weight is read once, N K / 2 bytes and the steps, for 2 M N K operations.  What bounds it is not that memory but
+// turning codes into operands, eleven instructions for eight codes (seven of them integer).  So the product runs on
+// the warp-level tensor core instruction with the weight as the 16-row operand: a conversion serves 8 tokens at once.
+// One bf16 token: 4096 x 4096 in 4.4 us, 11008 x 4096 in 8.8 (2.9 TB/s); 8 tokens, 4096 x 22016: 16.4 us (2.9 TB/s), the
+// SMs issuing in 57 % of their cycles; 3 fp32 tokens, 4099 x 11007: 19.9 us.
 //   - Codes in -7 .. 7 are exact in bf16, and bf16 entries of X are operands as they are.
 //   - An fp32 entry is cut into three bf16 parts of 8 bits, exact together: a column of the other operand for each
 //     part with up to 2 tokens, an operand for each part with more.
 //   - The sums of a group are scaled by its step in fp32.
 // A CTA takes 16 kR output channels at a time; its eight warps take the blocks of 128 inputs in turn, each with its own
 // ring of asynchronous copies that runs on from one set of channels to the next.  The warps' sums meet in shared
-// memory, in a fixed order.
+// memory, in a fixed order.  (X read straight into registers, a block ahead, cost 17.1 us for the 8 tokens.)
 struct MatvecArgs {
   const uint8_t* codes;
   int64_t ldc;
@@ -352,7 +359,8 @@ struct MvShape {
   static constexpr int kPerBlock = kBlock / kGroup;           // steps of a row and block
   static constexpr int kXAt = 2 * kR * 512, kStepsAt = kXAt + kXRows * kXPitch;
   static constexpr int kStage = kStepsAt + 2 * kR * 8 * kPerBlock * 4;
-  static constexpr int kPerSm = kTiles * kR <= 2 ? 2 : 1;     // CTAs an SM, by registers
+  // CTAs an SM: two where registers allow (8 tokens, 4096 x 22016: 16.4 us; with one and rings twice as long 18.8)
+  static constexpr int kPerSm = kTiles * kR <= 2 ? 2 : 1;
   static constexpr int kCols = kTiles * 8;
   static constexpr int kRed = kMvWarps * 16 * kR * kCols * 4;
   // where a row's and column's sum of a warp lies: turned by a place every four rows, against bank conflicts
@@ -417,19 +425,21 @@ __global__ void __launch_bounds__(kMvWarps * 32, MvShape<T, kGroup, kTiles, kR>:
       const uint32_t dst = smem_addr(to), dst_x = dst + S::kXAt;
 #pragma unroll
       for (int r = 0; r < 2 * kR; ++r) cp_async<16>(dst + lane * 16 + r * 512, code_row[r] + (uint32_t)kb_in * kBlockBytes);
-      if (kb_in * kPerBlock + lane % kPerBlock < groups) {
+      // zeros for groups behind the last one: no stale step meets their sums of 0
+      const uint32_t step_bytes = kb_in * kPerBlock + lane % kPerBlock < groups ? 4u : 0u;
 #pragma unroll
-        for (int q = 0; q < kStepCopies; ++q)
-          if (16 * kR * kPerBlock >= 32 || lane < 16 * kR * kPerBlock)
-            cp_async<4>(dst + S::kStepsAt + (q * 32 + lane) * 4, step_row[q] + (uint32_t)kb_in * kPerBlock);
-      }
+      for (int q = 0; q < kStepCopies; ++q)
+        if (16 * kR * kPerBlock >= 32 || lane < 16 * kR * kPerBlock)
+          cp_async_part<4>(dst + S::kStepsAt + (q * 32 + lane) * 4, step_bytes ? step_row[q] + (uint32_t)kb_in * kPerBlock : a.steps,
+                           step_bytes);
       const uint32_t k_bytes = (uint32_t)kb_in * (kBlock * (int)sizeof(T));
       if (kb_in < whole16) {
         const uint8_t* row = x16 + k_bytes;
 #pragma unroll
         for (int q = 0; q < S::kXRows / kRowsAtOnce; ++q) {
           if (q * kRowsAtOnce >= tokens) break;
-          if (kRowsAtOnce == 1 || q * kRowsAtOnce + lane / kRowLanes < tokens) cp_async<16>(dst + (to16 ^ (kRowsAtOnce == 1 ? q % 2 * S::kSwap : 0)) + q * kRowsAtOnce * S::kXPitch, row);
+          const uint32_t at = (to16 ^ (kRowsAtOnce == 1 ? q % 2 * S::kSwap : 0)) + q * kRowsAtOnce * S::kXPitch;
+          if (kRowsAtOnce == 1 || q * kRowsAtOnce + lane / kRowLanes < tokens) cp_async<16>(dst + at, row);
           row += kRowsAtOnce * row_bytes;
         }
       } else if (a.aligned >= 4 && kb_in < whole) {  // rows that begin anywhere: four bytes at a time
@@ -455,12 +465,15 @@ __global__ void __launch_bounds__(kMvWarps * 32, MvShape<T, kGroup, kTiles, kR>:
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              v[j][q] = k0 + 32 * q < K ? *reinterpret_cast<const T*>(x0 + min(t + j, tokens - 1) * row_bytes + (k0 + 32 * q) * (int64_t)sizeof(T))
+              v[j][q] = k0 + 32 * q < K ? reinterpret_cast<const T*>(x0 + min(t + j, tokens - 1) * row_bytes)[k0 + 32 * q]
                                         : from_f32<T>(0.f);
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) *reinterpret_cast<T*>(to + S::kXAt + (t + j) * S::kXPitch + ((32 * q + lane) * (int)sizeof(T) ^ j * S::kSwap)) = v[j][q];
+            for (int q = 0; q < 4; ++q) {
+              const int at = (32 * q + lane) * (int)sizeof(T) ^ j * S::kSwap;
+              *reinterpret_cast<T*>(to + S::kXAt + (t + j) * S::kXPitch + at) = v[j][q];
+            }
         }
       }
       stage_in = stage_in + 1 == kStages ? 0 : stage_in + 1;

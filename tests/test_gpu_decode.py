@@ -178,6 +178,37 @@ def test_matvec(imq, K, N, group, M, xt, yt):
     assert torch.equal(y, imq.imq_w4_matvec(w, X, out_dtype=yt))  # the same bits again
 
 
+@pytest.mark.parametrize("xt,yt", [(torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32)])
+@pytest.mark.parametrize("M", [1, 2, 3, 8, 9, 16, 17])
+@pytest.mark.parametrize("K,N,group", [(514, 2369, 32), (130, 10007, 64), (2049, 4737, 128)])
+def test_matvec_of_many_channels(imq, K, N, group, M, xt, yt):
+    """More channels than the SMs hold at once; rows of X on 4-byte and, in bf16, on 2-byte boundaries."""
+    W = _randn(K + N + 1, N, K, heavy=30.0)
+    X = _randn(M + 1, M, K, dtype=xt, heavy=60.0)
+    w = imq.imq_w4_quantize(W, group, transW=True)
+    y = imq.imq_w4_matvec(w, X, out_dtype=yt)
+    want, tol = matvec_bound(plain_weight_codes(w.codes, K), w.steps.cpu().numpy(), group, f64(X), M, xt == torch.float32)
+    tol = tol + HALF_STEP[yt] * (np.abs(want) + tol)
+    assert (np.abs(f64(y) - want) <= tol).all()
+    assert torch.equal(y, imq.imq_w4_matvec(w, X, out_dtype=yt))
+
+
+@leaves(2)
+@pytest.mark.parametrize("xt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M", [1, 3, 9])
+@pytest.mark.parametrize("K,N,group", [(130, 300, 64), (514, 5000, 32), (33, 40, 32)])
+def test_matvec_after_values_that_are_not_finite(imq, K, N, group, M, xt):
+    """A last block with fewer groups than others, where steps and tokens that are NaN were multiplied before."""
+    bad = imq.imq_w4_quantize(torch.full((N, 1024), float("nan"), device="cuda"), group, transW=True)
+    w = imq.imq_w4_quantize(_randn(3, N, K), group, transW=True)
+    X = _randn(4, M, K, dtype=xt)
+    for _ in range(3):
+        assert torch.isnan(imq.imq_w4_matvec(bad, torch.full((16, 1024), float("nan"), device="cuda", dtype=xt)[:M])).all()
+        y = imq.imq_w4_matvec(w, X, out_dtype=torch.float32)
+        want, tol = matvec_bound(plain_weight_codes(w.codes, K), w.steps.cpu().numpy(), group, f64(X), M, xt == torch.float32)
+        assert (np.abs(f64(y) - want) <= tol + HALF_STEP[torch.float32] * (np.abs(want) + tol)).all()
+
+
 def test_matvec_of_nothing(imq):
     w = imq.imq_w4_quantize(_randn(1, 0, 24), 32)
     assert (w.K, w.N) == (0, 24)
