@@ -512,7 +512,8 @@ imq_status imq_w4_dequantize(const uint8_t *codes, int64_t ldc, const float *ste
  * tokens use the GEMM above.  The order of the sums is fixed: equal inputs give equal bits.
  * X       device, M x K, dtype xt (F32 or BF16), leading dimension ldx (>= K).  fp32 entries keep all their
  *         bits.  A non-finite entry gives its token non-finite outputs.
- * Y       device, M x N, dtype yt (F32 or BF16), leading dimension ldy (>= N).  K = 0 gives zeros.
+ * Y       device, M x N, dtype yt (F32 or BF16), leading dimension ldy (>= N).  K = 0 gives zeros.  Must not
+ *         overlap X.
  * Errors: IMQ_ERR_ARG; IMQ_ERR_UNSUPPORTED for M above 1 048 560.
  */
 imq_status imq_w4_matvec(const uint8_t *codes, int64_t ldc, const float *steps, int64_t lds, int64_t K, int64_t N,
@@ -544,7 +545,7 @@ typedef struct {
  *         not negative), head_dim consecutive entries.
  * slots   device int64[n], 8-byte aligned: the slot of each token; a negative one is skipped (padding).
  *         The slots of one call must differ; of two tokens on one slot it is not defined which one's
- *         codes and steps are kept.  A slot outside the cache is skipped and sets IMQ_ERR_BOUNDS in the
+ *         codes and steps are kept, and they may be of different tokens.  A slot outside the cache is skipped and sets IMQ_ERR_BOUNDS in the
  *         status word.  IMQ_ERR_UNSUPPORTED for n * heads of 2^31 or more.
  */
 imq_status imq_kv_write(const imq_kv_cache *cache, const void *K, int64_t k_token_stride, int64_t k_head_stride,
@@ -571,7 +572,8 @@ imq_status imq_paged_attention_workspace(const imq_kv_cache *cache, int64_t batc
  *   lse[b, h] = log sum_t exp(s_t)
  * Scores, softmax statistics and sums are fp32.  Codes enter the products exactly; a query entry as an integer
  * multiple of 2^-23 of its row's largest (a row below 1e-30 counts as zeros); a probability times its
- * value's step with 22 bits, or to 2^-36 of the largest where that is more.  The order of the sums is fixed: equal inputs give equal bits.
+ * value's step with 22 bits, or to 2^-36 of the largest where that is more.  The order of the sums is fixed: equal
+ * inputs give equal bits.
  * Q           device, dtype qt (F32 or BF16): sequence b, head h at b * q_batch_stride + h * q_head_stride, head_dim
  *             consecutive entries.  A non-finite query gives NaN.
  * block_table device int32, batch rows of table_stride entries: entry j of a row is the page of tokens
@@ -581,8 +583,8 @@ imq_status imq_paged_attention_workspace(const imq_kv_cache *cache, int64_t batc
  * max_len     no sequence is longer (at most table_width * page_size); it sizes the launch.  A longer sequence
  *             has out and lse NaN and sets IMQ_ERR_BOUNDS in the status word; so has one whose page lies outside
  *             the cache.
- * out         device, dtype ot (F32 or BF16), addressed as Q.   lse: device fp32 or NULL, row b at
- *             b * lse_batch_stride.
+ * out         device, dtype ot (F32 or BF16), addressed as Q; must not overlap it.   lse: device fp32 or NULL, row b
+ *             at b * lse_batch_stride.
  * workspace   device, 16-byte aligned, at least imq_paged_attention_workspace bytes (IMQ_ERR_BUFFER otherwise); need
  *             not be initialised.  Calls whose executions overlap, and graphs that replay at the same time,
  *             need workspaces of their own.
