@@ -444,10 +444,11 @@ __global__ void __launch_bounds__(kMvWarps * 32, MvShape<T, kGroup, kTiles, kR>:
         }
       } else if (a.aligned >= 4 && kb_in < whole) {  // rows that begin anywhere: four bytes at a time
         const uint8_t* row = x0 + k_bytes + lane * 4;
-        uint32_t at = dst_x + lane * 4;
+        uint32_t at = dst_x;
         for (int t = 0; t < tokens; ++t, row += row_bytes, at += S::kXPitch) {
+          const uint32_t to4 = at + (lane * 4 ^ t % 2 * S::kSwap);  // (stages begin at multiples of 64 bytes: not at ^ ...)
 #pragma unroll
-          for (int q = 0; q < kBlock * (int)sizeof(T) / 128; ++q) cp_async<4>((at ^ t % 2 * S::kSwap) + q * 128, row + q * 128);
+          for (int q = 0; q < kBlock * (int)sizeof(T) / 128; ++q) cp_async<4>(to4 + q * 128, row + q * 128);
         }
       } else if (a.aligned >= 4) {  // the end of a row, zeros behind it
         const int left = (K - kb_in * kBlock) * (int)sizeof(T);  // bytes

@@ -193,6 +193,21 @@ def test_matvec_of_many_channels(imq, K, N, group, M, xt, yt):
     assert torch.equal(y, imq.imq_w4_matvec(w, X, out_dtype=yt))
 
 
+@pytest.mark.parametrize("xt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("pad", [0, 1, 2, 4, 8])
+@pytest.mark.parametrize("M", [2, 3, 9, 12])
+@pytest.mark.parametrize("N,group", [(15, 32), (15, 64), (15, 128), (2400, 128)])
+def test_matvec_rows_on_any_boundary(imq, N, group, M, pad, xt):
+    """Rows of X that begin on multiples of 16, 8, 4 and 2 bytes, in every stage of the rings."""
+    K = 2056
+    W = _randn(9, N, K)
+    X = _randn(10, M, K + pad, dtype=xt)[:, pad:]
+    w = imq.imq_w4_quantize(W, group, transW=True)
+    y = imq.imq_w4_matvec(w, X, out_dtype=torch.float32)
+    want, tol = matvec_bound(plain_weight_codes(w.codes, K), w.steps.cpu().numpy(), group, f64(X), M, xt == torch.float32)
+    assert (np.abs(f64(y) - want) <= tol + HALF_STEP[torch.float32] * (np.abs(want) + tol)).all()
+
+
 @leaves(2)
 @pytest.mark.parametrize("xt", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("M", [1, 3, 9])
