@@ -317,15 +317,15 @@ __global__ void __launch_bounds__(128) k_w4_dequantize_cols(DequantArgs a) {
 // The weight is read once, N K / 2 bytes and the steps, for 2 M N K operations.  What bounds it is not that memory but
 // turning codes into operands, eleven instructions for eight codes (seven of them integer).  So the product runs on
 // the warp-level tensor core instruction with the weight as the 16-row operand: a conversion serves 8 tokens at once.
-// One bf16 token: 4096 x 4096 in 4.4 us, 11008 x 4096 in 8.8 (2.9 TB/s); 8 tokens, 4096 x 22016: 16.4 us (2.9 TB/s), the
-// SMs issuing in 57 % of their cycles; 3 fp32 tokens, 4099 x 11007: 19.9 us.
+// One bf16 token: 4096 x 4096 in 4.3 us, 11008 x 4096 in 8.6 (2.9 TB/s); 8 tokens, 4096 x 22016: 16.0 us (3.0 TB/s), the
+// SMs issuing in 58 % of their cycles; 3 fp32 tokens, 4099 x 11007: 20.2 us.
 //   - Codes in -7 .. 7 are exact in bf16, and bf16 entries of X are operands as they are.
 //   - An fp32 entry is cut into three bf16 parts of 8 bits, exact together: a column of the other operand for each
 //     part with up to 2 tokens, an operand for each part with more.
 //   - The sums of a group are scaled by its step in fp32.
 // A CTA takes 16 kR output channels at a time; its eight warps take the blocks of 128 inputs in turn, each with its own
 // ring of asynchronous copies that runs on from one set of channels to the next.  The warps' sums meet in shared
-// memory, in a fixed order.  (X read straight into registers, a block ahead, cost 17.1 us for the 8 tokens.)
+// memory, in a fixed order.  (X read straight into registers, a block ahead, cost 17.1 us for the 8 tokens; 16.3 then.)
 struct MatvecArgs {
   const uint8_t* codes;
   int64_t ldc;
@@ -359,7 +359,7 @@ struct MvShape {
   static constexpr int kPerBlock = kBlock / kGroup;           // steps of a row and block
   static constexpr int kXAt = 2 * kR * 512, kStepsAt = kXAt + kXRows * kXPitch;
   static constexpr int kStage = kStepsAt + 2 * kR * 8 * kPerBlock * 4;
-  // CTAs an SM: two where registers allow (8 tokens, 4096 x 22016: 16.4 us; with one and rings twice as long 18.8)
+  // CTAs an SM: two where registers allow (8 tokens, 4096 x 22016: 16.0 us; with one and rings twice as long 18.8)
   static constexpr int kPerSm = kTiles * kR <= 2 ? 2 : 1;
   static constexpr int kCols = kTiles * 8;
   static constexpr int kRed = kMvWarps * 16 * kR * kCols * 4;
