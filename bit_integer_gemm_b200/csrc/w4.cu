@@ -80,23 +80,28 @@ __global__ void __launch_bounds__(256) k_w4_quantize_rows(QuantArgs a) {
   uint32_t key[kRows];
 #pragma unroll
   for (int j = 0; j < kRows; ++j) key[j] = max_key(x[j]);
-  for (int o = 1; o < 1 << (a.log_group - 3); o <<= 1)
+  const int lanes = 1 << (a.log_group - 3);  // of a group: 4, 8 or 16
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) key[j] = max(key[j], __shfl_xor_sync(0xffffffffu, key[j], o));
+  for (int o = 1; o < 16; o <<= 1)
+    if (o < lanes) {
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) key[j] = max(key[j], __shfl_xor_sync(0xffffffffu, key[j], o));
+    }
   float s[kRows], step[kRows];
   four_scales(key, 7.f, s, step);
   if (k - 8 * i >= K) return;  // the row's last block was the other half's
-  const bool writes_step = ((8 * i) & ((1 << a.log_group) - 1)) == 0 && k < K;
-  uint8_t* const to = a.codes + n0 * a.ldc + k0 / kBlock * kBlockBytes + (lane >> 4) * kBlockBytes + 4 * word_of(i);
-  float* const to_step = a.steps + n0 * a.lds + (k >> a.log_group);
+  const int rows = min(kRows, N - n0);
+  uint8_t* to = a.codes + n0 * a.ldc + k0 / kBlock * kBlockBytes + (lane >> 4) * kBlockBytes + 4 * word_of(i);
 #pragma unroll
-  for (int j = 0; j < kRows; ++j) {
-    if (n0 + j >= N) break;
-    *reinterpret_cast<uint32_t*>(to + j * a.ldc) = pack4(x[j], s[j]);
-    if (writes_step) {
-      to_step[j * a.lds] = step[j];
-      if (!key_finite(key[j])) set_status(a.status, IMQ_ERR_NONFINITE);
-    }
+  for (int j = 0; j < kRows; ++j, to += a.ldc)
+    if (j < rows) *reinterpret_cast<uint32_t*>(to) = pack4(x[j], s[j]);
+  if ((i & (lanes - 1)) == 0 && k < K) {
+    float* to_step = a.steps + n0 * a.lds + (k >> a.log_group);
+    bool finite = true;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j, to_step += a.lds)
+      if (j < rows) *to_step = step[j], finite &= key_finite(key[j]);
+    if (!finite) set_status(a.status, IMQ_ERR_NONFINITE);
   }
 }
 
