@@ -39,9 +39,10 @@ __device__ __forceinline__ uint32_t max_key(const float (&x)[8]) {
 }
 
 // Row kernels (W stored N x K): a warp takes 256 inputs (two blocks) of four rows, 8 inputs of each a lane.  Bound: memory
-// for fp32 (11003 x 4097 in 37.9 us, 5.4 TB/s, and back in 34.1), the quantiser's instructions for bf16 (4096 x 4096 in
-// 12.5 us, 3.4 TB/s; back 9.1).
+// for fp32 (11003 x 4097 in 36.4 us, 5.7 TB/s, and back in 34.1), the quantiser's instructions for bf16 (4096 x 4096 in
+// 11.9 us, 3.6 TB/s; back 9.1).
 constexpr int kRows = 4;
+constexpr int kQuantWarps = 4;  // of the quantiser's CTAs (8: 37.6 us and 12.0)
 
 // x[e] = entry e * 32 + lane of 256 consecutive ones, becomes entry 8 * lane + e: turned in shared memory (`turn`, 288
 // floats of the warp's own, a float of padding every 8 entries).
@@ -55,10 +56,10 @@ __device__ __forceinline__ void turn256(float* turn, int lane, float (&x)[8]) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) k_w4_quantize_rows(QuantArgs a) {
-  __shared__ float s_turn[8][288];
+__global__ void __launch_bounds__(kQuantWarps * 32) k_w4_quantize_rows(QuantArgs a) {
+  __shared__ float s_turn[kQuantWarps][288];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = lane & 15;
-  const uint32_t per_row = ((uint32_t)a.K + 255) / 256, unit = blockIdx.x * 8 + warp;
+  const uint32_t per_row = ((uint32_t)a.K + 255) / 256, unit = blockIdx.x * kQuantWarps + warp;
   const int n0 = (int)(unit / per_row) * kRows, k0 = (int)(unit % per_row) * 256, k = k0 + 8 * lane;
   const int N = (int)a.N, K = (int)a.K;
   if (n0 >= N) return;
@@ -689,12 +690,12 @@ imq_status launch_w4_quantize(const void* W, imq_dtype wt, int64_t K, int64_t N,
   if (s != IMQ_OK) return s;
   QuantArgs a{W, K, N, ldw, codes, ldc, steps, lds, log2_of(group), vectors(W, ldw, wt, transW), ds->status};
   if (transW) {
-    const int64_t ctas = ((N + kRows - 1) / kRows * ((K + 255) / 256) + 7) / 8;
+    const int64_t ctas = ((N + kRows - 1) / kRows * ((K + 255) / 256) + kQuantWarps - 1) / kQuantWarps;
     if (ctas > INT32_MAX / 8) return IMQ_ERR_UNSUPPORTED;
     if (wt == IMQ_F32)
-      k_w4_quantize_rows<float><<<(unsigned)ctas, 256, 0, st>>>(a);
+      k_w4_quantize_rows<float><<<(unsigned)ctas, kQuantWarps * 32, 0, st>>>(a);
     else
-      k_w4_quantize_rows<__nv_bfloat16><<<(unsigned)ctas, 256, 0, st>>>(a);
+      k_w4_quantize_rows<__nv_bfloat16><<<(unsigned)ctas, kQuantWarps * 32, 0, st>>>(a);
   } else {
     const int64_t nb = (K + kBlock - 1) / kBlock;
     if (nb > 65535) return IMQ_ERR_UNSUPPORTED;
