@@ -251,9 +251,11 @@ __global__ void __launch_bounds__(256) k_w4_dequantize_rows(DequantArgs a) {
     float x[8];
     word_values(w[j], step[j], a.one, x);
     const bool whole = a.vec && k0 + 256 <= K;
-    if (sizeof(T) == 2 && whole) {  // 16 bytes a lane, in order
-      store8(out + j * a.ldw + 8 * lane, x);
-      continue;
+    if constexpr (sizeof(T) == 2) {
+      if (whole) {  // 16 bytes a lane, in order
+        store8(out + j * a.ldw + 8 * lane, x);
+        continue;
+      }
     }
     __syncwarp();
 #pragma unroll
@@ -464,7 +466,7 @@ __global__ void __launch_bounds__(kMvWarps * 32, MvShape<T, kGroup, kTiles, kR>:
             cp_async_part<4>(dst_x + t * S::kXPitch + (at ^ t % 2 * S::kSwap), n ? x0 + t * row_bytes + k_bytes + at : a.codes, n);
           }
         }
-      } else {
+      } else if constexpr (!S::kF32) {  // bf16 rows on 2-byte boundaries
         const int k0 = kb_in * kBlock + lane;
         for (int t = 0; t < tokens; t += 2) {  // (loads of two rows under way together)
           T v[2][4];
