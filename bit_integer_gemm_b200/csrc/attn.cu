@@ -15,16 +15,18 @@
 //     conversion, 4-bit codes three instructions for eight.  Rows g and g + 8 of one 16-row operand hold the
 //     first two digits of up to 8 query heads, a second operand the third; for 9 to 16 heads each digit has
 //     an operand.
-//   - p * v runs on fp16 with fp32 sums: codes are exact in fp16; a probability times its value's step, in units
-//     of the largest step so far and of 2^-11, is cut into two fp16 parts, 22 bits together.  With up to 8
-//     query heads both parts share one 16-row operand, so the second costs no further instruction.
+//   - p * v runs on fp16 with fp32 sums: codes are exact in fp16; a probability times its value's step, the weight
+//     of a code, is cut into two fp16 parts, 22 bits together, in units of the query head's largest weight so far and
+//     of 2^-11.  So what a weight loses is at most 2^-36 of the largest of its head.  With up to 8 query heads both
+//     parts share one 16-row operand, so the second costs no further instruction.
 // The inner axis of a product may be permuted at will if both operands agree, so a lane's 16 (or 8) bytes of a
 // key are contiguous ones.  Values are transposed on the way from shared memory (pairs of bytes, or four
 // nibbles, of two tokens to a register), and the columns they make are sorted out when the sums are written.
 //
-// The softmax keeps a reference instead of the running maximum: it is raised (and the sums rescaled) only when a
-// weight exceeds it 8 times, or a value's step the unit of steps twice (together the room that fp16 leaves above
-// 2^11), so most runs need no exchange between lanes.
+// The softmax keeps a reference instead of the running maximum, and so does the unit of the weights: they are raised
+// (and the sums rescaled) only when an exponential exceeds the reference's 8 times, or a weight the unit 16 times (the
+// room that fp16 leaves above 2^11), so most runs need no exchange between lanes.  A vector of zeros has the step 1
+// whatever the others have; it adds nothing, and the unit leaves it out.
 //
 // Split: the work of all sequences and key heads lies in one line of units of 64 tokens, cut into equal parts, one
 // for each CTA that the SMs hold at once; so lengths may differ as they will.  A row (one sequence's tokens of one key
@@ -54,10 +56,10 @@ constexpr int kRun = 16;              // tokens that a warp copies at a time; th
 constexpr int kUnit = kWarps * kRun;  // tokens: the grain of the split
 constexpr uint32_t kRowCost = 4;      // what a row costs besides its units, in units
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 3.f;          // how far, in powers of two, a weight may exceed the reference's,
-constexpr float kStepSlack = 2.f;      // and how many times a step the unit of steps
-constexpr float kPScale = 2048.f;      // unit of the weights in fp16: 2^15 is the largest
-constexpr float kStepFloor = 1e-30f;   // the unit of the steps starts here
+constexpr float kSlack = 8.f;          // how many times an exponential may exceed the reference's
+constexpr float kPScale = 2048.f;      // the unit of the weights in fp16,
+constexpr float kPMost = 32768.f;      // and the largest weight
+constexpr float kUnitFloor = 1e-33f;   // the unit of the weights starts here
 constexpr float kQMax = 8355700.f;     // the largest query entry: below 127 * 65536 + 127 * 256 + 127 by more than its rounding
 
 struct AttnArgs {
@@ -211,6 +213,7 @@ template <int kBits, int kD, int kM>
 struct Shape {
   using KP = Pieces<kBits, kD>;
   static constexpr int kRow = kD * kBits / 8, kChunks = kRow / 16;
+  static constexpr uint32_t kZeros = kBits == 8 ? 0x80808080u : 0x88888888u;  // codes of 0
   // Values lie in rows of 16-byte chunks; eight rows' chunks of one column are in different banks: by an exclusive or
   // of the chunk with the row where a row is a power of two, by a chunk of padding where it is not.
   static constexpr bool kPadded = (kRow & (kRow - 1)) != 0;
@@ -318,6 +321,19 @@ struct Query {
     }
   }
 };
+
+// A bit for each of a run's 16 value vectors that has a code other than 0.
+template <typename S>
+__device__ __forceinline__ uint32_t nonzero_rows(const uint8_t* values, int lane) {
+  uint32_t rows = 0;
+#pragma unroll
+  for (int q = 0; q < S::kChunks / 2; ++q) {
+    const int at = q * 32 + lane, row = at / S::kChunks;
+    const uint4 v = *reinterpret_cast<const uint4*>(values + S::chunk_at(row, at % S::kChunks));
+    if (((v.x ^ S::kZeros) | (v.y ^ S::kZeros) | (v.z ^ S::kZeros) | (v.w ^ S::kZeros)) != 0u) rows |= 1u << row;
+  }
+  return __reduce_or_sync(0xffffffffu, rows);
+}
 
 template <int kBits, int kD, int kM>
 __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_attn(const __grid_constant__ AttnArgs a) {
@@ -540,9 +556,11 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
 
     // ---- the warp's runs
     float o[S::kCols][4] = {};
-    float m[kM], l[kM], vref = kStepFloor, winv = kPScale / kStepFloor;
+    // of a head: the reference's exponent, the sum of the exponentials, and the unit of the weights (of an exponential of 1
+    // and a step of 1)
+    float m[kM], l[kM], wunit[kM], winv[kM];
 #pragma unroll
-    for (int r = 0; r < kM; ++r) m[r] = minus_inf(), l[r] = 0.f;
+    for (int r = 0; r < kM; ++r) m[r] = minus_inf(), l[r] = 0.f, wunit[r] = kUnitFloor, winv[r] = kPScale / kUnitFloor;
     const uint8_t* run = ring + warp * S::kRing;
 
 #pragma unroll 1
@@ -552,7 +570,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
       issue(u + kStages - 1);
       // ---- scores, two blocks of eight tokens; this lane's tokens are 2c, 2c + 1, 2c + 8, 2c + 9, its heads g (and g + 8)
       constexpr int kMine = 4;
-      float p[kM][kMine];
+      float x[kM][kMine];
       {
         int32_t acc[2][S::kQOps][4] = {};
         uint32_t w[2][KP::kBytes / 4];
@@ -576,11 +594,11 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
         for (int r = 0; r < kM; ++r)
 #pragma unroll
           for (int j = 0; j < kMine; ++j) {
-            const auto& x = acc[j >> 1];
-            const int32_t d0 = kM == 1 ? x[0][j & 1] : x[0][2 * r + (j & 1)];
-            const int32_t d1 = kM == 1 ? x[0][2 + (j & 1)] : x[kM - 1][2 * r + (j & 1)];
-            const int32_t d2 = kM == 1 ? x[1][j & 1] : x[kM][2 * r + (j & 1)];
-            p[r][j] = fmaf((float)(d0 * 256 + d1 + start[0][r]), 256.f, (float)(d2 + start[1][r]));
+            const auto& sum = acc[j >> 1];
+            const int32_t d0 = kM == 1 ? sum[0][j & 1] : sum[0][2 * r + (j & 1)];
+            const int32_t d1 = kM == 1 ? sum[0][2 + (j & 1)] : sum[kM - 1][2 * r + (j & 1)];
+            const int32_t d2 = kM == 1 ? sum[1][j & 1] : sum[kM][2 * r + (j & 1)];
+            x[r][j] = fmaf((float)(d0 * 256 + d1 + start[0][r]), 256.f, (float)(d2 + start[1][r]));
           }
       }
       float ks[kMine], vs[kMine];
@@ -589,46 +607,71 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
         const float4 st = *reinterpret_cast<const float4*>(run + S::kStepsAt + j * 64 + c * 16);
         ks[2 * j] = st.x, vs[2 * j] = st.y, ks[2 * j + 1] = st.z, vs[2 * j + 1] = st.w;
       }
-      float vmax = vs[0];
-#pragma unroll
-      for (int j = 1; j < kMine; ++j) vmax = fmaxf(vmax, vs[j]);
-      bool raise = vmax > kStepSlack * vref;
 #pragma unroll
       for (int r = 0; r < kM; ++r)
 #pragma unroll
-        for (int j = 0; j < kMine; ++j) p[r][j] *= ks[j] * mul[r];
+        for (int j = 0; j < kMine; ++j) x[r][j] *= ks[j] * mul[r];
       const int left = end - (first + u * kUnit);
       if (left < kRun) {
 #pragma unroll
         for (int j = 0; j < kMine; ++j)
           if (8 * (j >> 1) + 2 * c + (j & 1) >= left) {
 #pragma unroll
-            for (int r = 0; r < kM; ++r) p[r][j] = minus_inf();
+            for (int r = 0; r < kM; ++r) x[r][j] = minus_inf();
           }
       }
-      float top[kM];
+      // ---- exponentials, and the weights of the codes
+      float p[kM][kMine], wt[kM][kMine];
+      bool raise = false;
 #pragma unroll
       for (int r = 0; r < kM; ++r) {
-        top[r] = p[r][0];
+        float pmax = 0.f, wmax = 0.f;
 #pragma unroll
-        for (int j = 1; j < kMine; ++j) top[r] = fmaxf(top[r], p[r][j]);
-        raise |= top[r] > m[r] + kSlack;
+        for (int j = 0; j < kMine; ++j) {
+          p[r][j] = ex2(x[r][j] - m[r]);
+          wt[r][j] = p[r][j] * vs[j] * winv[r];
+          pmax = fmaxf(pmax, p[r][j]), wmax = fmaxf(wmax, wt[r][j]);
+        }
+        raise |= pmax > kSlack || wmax > kPMost;
       }
       if (__any_sync(0xffffffffu, raise)) {
-        // new references, the largest so far, and the sums in their units
+        // vectors of zeros: their step of 1 is no weight
+        bool one = false;
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) one |= vs[j] == 1.f;
+        if (__any_sync(0xffffffffu, one)) {
+          const uint32_t live = nonzero_rows<S>(run + S::kValues, lane);
+#pragma unroll
+          for (int j = 0; j < kMine; ++j)
+            if (vs[j] == 1.f && !(live >> (8 * (j >> 1) + 2 * c + (j & 1)) & 1)) vs[j] = 0.f;
+        }
+        // new references and units, the largest so far, and the sums in their terms
         float fix[kM];
-        vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
-        vmax = fmaxf(fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2)), vref);
-        const float ratio = __fdividef(vref, vmax);
-        vref = vmax, winv = __fdividef(kPScale, vmax);
 #pragma unroll
         for (int r = 0; r < kM; ++r) {
-          top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-          top[r] = fmaxf(fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2)), m[r]);
-          const float alpha = top[r] == minus_inf() ? 1.f : ex2(m[r] - top[r]);  // (no score yet but NaN)
-          m[r] = top[r];
+          float top = x[r][0];
+#pragma unroll
+          for (int j = 1; j < kMine; ++j) top = fmaxf(top, x[r][j]);
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)), m[r]);
+          const float alpha = top == minus_inf() ? 1.f : ex2(m[r] - top);  // (no score yet but NaN)
+          m[r] = top;
           l[r] *= alpha;
-          fix[r] = alpha * ratio;
+          float most = 0.f;
+#pragma unroll
+          for (int j = 0; j < kMine; ++j) {
+            p[r][j] = ex2(x[r][j] - top);
+            wt[r][j] = p[r][j] * vs[j];
+            most = fmaxf(most, wt[r][j]);
+          }
+          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+          const float old = wunit[r] * alpha;
+          wunit[r] = fmaxf(fmaxf(most, old), kUnitFloor);
+          fix[r] = __fdividef(old, wunit[r]);
+          winv[r] = __fdividef(kPScale, wunit[r]);
+#pragma unroll
+          for (int j = 0; j < kMine; ++j) wt[r][j] *= winv[r];
         }
         if (u > 0) {
 #pragma unroll
@@ -639,20 +682,14 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
         }
       }
 #pragma unroll
-      for (int j = 0; j < kMine; ++j) {
-        const float vw = vs[j] * winv;
+      for (int r = 0; r < kM; ++r)
 #pragma unroll
-        for (int r = 0; r < kM; ++r) {
-          p[r][j] = ex2(p[r][j] - m[r]);
-          l[r] += p[r][j];
-          p[r][j] *= vw;
-        }
-      }
+        for (int j = 0; j < kMine; ++j) l[r] += p[r][j];
       uint32_t hi[kM][2], lo[kM][2];  // weights as operands
 #pragma unroll
       for (int r = 0; r < kM; ++r) {
-        split_f16(p[r][0], p[r][1], &hi[r][0], &lo[r][0]);
-        split_f16(p[r][2], p[r][3], &hi[r][1], &lo[r][1]);
+        split_f16(wt[r][0], wt[r][1], &hi[r][0], &lo[r][0]);
+        split_f16(wt[r][2], wt[r][3], &hi[r][1], &lo[r][1]);
       }
       auto product = [&](float (&acc)[4], uint32_t b0, uint32_t b1) {
         if (kM == 1) {
@@ -701,7 +738,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
       float top = s_m[0][g + 8 * r];
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w][g + 8 * r]);
-      const float weight = top == minus_inf() ? 1.f : ex2(m[r] - top), f = weight * (vref * (1.f / kPScale));
+      const float weight = top == minus_inf() ? 1.f : ex2(m[r] - top), f = weight * (wunit[r] * (1.f / kPScale));
       if (c == 0) s_l[warp][g + 8 * r] = bad ? quiet_nan() : l[r] * weight;
       float* const row = sums + (warp * S::kHeads + g + 8 * r) * S::kPad;
 #pragma unroll

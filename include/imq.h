@@ -572,7 +572,8 @@ imq_status imq_paged_attention_workspace(const imq_kv_cache *cache, int64_t batc
  *   lse[b, h] = log sum_t exp(s_t)
  * Scores, softmax statistics and sums are fp32.  Codes enter the products exactly; a query entry as an integer
  * multiple of 2^-23 of its row's largest (a row below 1e-30 counts as zeros); a probability times its
- * value's step with 22 bits, or to 2^-36 of the largest where that is more.  The order of the sums is fixed: equal
+ * value's step with 22 bits, or to 2^-36 of the largest such product of its query head where that is more (the step 1 of
+ * a vector of zeros aside: it adds nothing and costs the others nothing).  The order of the sums is fixed: equal
  * inputs give equal bits.
  * Q           device, dtype qt (F32 or BF16): sequence b, head h at b * q_batch_stride + h * q_head_stride, head_dim
  *             consecutive entries.  A non-finite query gives NaN.
