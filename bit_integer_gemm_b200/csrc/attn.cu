@@ -8,13 +8,14 @@
 // query heads -- memory, far below the tensor cores' rate, but above what the fp32 units do at 8 query heads a
 // key head.  So both products run on warp-level tensor-core instructions, whose operands are registers: the
 // codes go from the copy to the operand without another trip through shared memory.
-//   - q * k runs on integers, exactly: a query row is scaled so that its largest entry becomes nearly 2^23 and
-//     rounded to an integer of three digits of radix 256 in -128 .. 127 (the unpacking of this library, applied
-//     to the query), and the stored bytes or nibbles are the other operand as they lie, offset and
+//   - q * k runs on integers, exactly: a query row is scaled by a power of two so that its largest entry lies between
+//     2^30 and 2^31, and rounded to integers of four digits of radix 256 in -128 .. 127 (the unpacking of this library,
+//     applied to the query), and the stored bytes or nibbles are the other operand as they lie, offset and
 //     all: the offset times the sum of a row's digits is what the sums start from.  8-bit codes need no
 //     conversion, 4-bit codes three instructions for eight.  Rows g and g + 8 of one 16-row operand hold the
-//     first two digits of up to 8 query heads, a second operand the third; for 9 to 16 heads each digit has
-//     an operand.
+//     first two digits of up to 8 query heads, a second operand the others; for 9 to 16 heads each digit has
+//     an operand.  (One query entry 1000 times as large as the others, on keys that are small there, costs
+//     the output 3e-7; with three digits it cost 4e-5.)
 //   - p * v runs on fp16 with fp32 sums: codes are exact in fp16; a probability times its value's step, the weight
 //     of a code, is cut into two fp16 parts, 22 bits together, in units of the query head's largest weight so far and
 //     of 2^-11.  So what a weight loses is at most 2^-36 of the largest of its head.  With up to 8 query heads both
@@ -60,7 +61,7 @@ constexpr float kSlack = 8.f;          // how many times an exponential may exce
 constexpr float kPScale = 2048.f;      // the unit of the weights in fp16,
 constexpr float kPMost = 32768.f;      // and the largest weight
 constexpr float kUnitFloor = 1e-33f;   // the unit of the weights starts here
-constexpr float kQMax = 8355700.f;     // the largest query entry: below 127 * 65536 + 127 * 256 + 127 by more than its rounding
+constexpr int kDigits = 4;              // of a query entry
 
 struct AttnArgs {
   imq_kv_cache c;
@@ -233,7 +234,7 @@ struct Shape {
   // 8 key heads at 8 bits, four 55.
   static constexpr int kPerSm = kD <= 64 ? 4 : kD <= 128 ? 3 : 2;
   static constexpr int kHeads = 8 * kM;
-  static constexpr int kQOps = kM + 1;                 // operands of the digits, 512 bytes each a step
+  static constexpr int kQOps = kDigits / 2 * kM;       // operands of the digits, 512 bytes each a step
   static constexpr int kQBytes = kSteps * kQOps * 512;
   static constexpr int kPad = kD + 4;
   static constexpr int kJoin = kWarps * kHeads * kPad * 4;  // the warps' sums, over the ring
@@ -275,27 +276,30 @@ struct Query {
       // a row of (almost) zeros, and one that is not finite (its scores' factor is NaN), have digits of 0
       const float top = __uint_as_float(key);
       const bool use = key_finite(key) && top > 1e-30f;
-      const float r = use ? __fdividef(kQMax / 16.f, top * (1.f / 16.f)) : 0.f;  // (that division is 0 from 2^126 on)
-      int32_t sum[3] = {};
+      // e: the exponent (and its offset of 127) of the largest entry, one more where its first digit would pass 127.  The
+      // entries are scaled by 2^(30 - (e - 127)) in two factors that fp32 has, without rounding.
+      const int e = (int)((key + 0x20000u) >> 23);
+      const float r = __int_as_float((260 - e) << 23);
+      int32_t sum[kDigits] = {};
 #pragma unroll
       for (int p = 0; p < kParts; ++p) {
         const int d = 4 * lane + 128 * p;
         if (kD % 128 != 0 && d >= kD) continue;
-        // v + 128 * (65536 + 256 + 1) has the digits, each plus 128, as its bytes
+        // v + 128 * (2^24 + 2^16 + 2^8 + 1) has the digits, each plus 128, as its bytes
         uint32_t u[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) u[j] = (uint32_t)__float2int_rn(use ? fminf(fmaxf(x[n][p][j] * r, -kQMax), kQMax) : 0.f) + 0x808080u;
+        for (int j = 0; j < 4; ++j) u[j] = (uint32_t)__float2int_rn(use ? x[n][p][j] * r * 16777216.f : 0.f) + 0x80808080u;
         const uint32_t a = __byte_perm(u[0], u[1], 0x5140), b = __byte_perm(u[2], u[3], 0x5140);
-        const uint32_t e = __byte_perm(u[0], u[1], 0x0062), f = __byte_perm(u[2], u[3], 0x0062);
-        // first, second, third digits of the four entries
-        const uint32_t dig[3] = {__byte_perm(e, f, 0x5410) ^ 0x80808080u, __byte_perm(a, b, 0x7632) ^ 0x80808080u,
-                                 __byte_perm(a, b, 0x5410) ^ 0x80808080u};
+        const uint32_t y = __byte_perm(u[0], u[1], 0x7362), z = __byte_perm(u[2], u[3], 0x7362);
+        // first to fourth digits of the four entries
+        const uint32_t dig[kDigits] = {__byte_perm(y, z, 0x7632) ^ 0x80808080u, __byte_perm(y, z, 0x5410) ^ 0x80808080u,
+                                       __byte_perm(a, b, 0x7632) ^ 0x80808080u, __byte_perm(a, b, 0x5410) ^ 0x80808080u};
         int c, w;
         S::KP::find(d, &c, &w);
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
+        for (int k = 0; k < kDigits; ++k) {
           sum[k] = __dp4a((int)dig[k], 0x01010101, sum[k]);
-          // kM = 1: operand 0 holds the first digit in row g and the second in row g + 8, operand 1 the third in row g;
+          // kM = 1: operand 0 holds the first digit in row g and the second in row g + 8, operand 1 the third and fourth;
           // kM = 2: an operand a digit, heads g and g + 8
           const int op = kM == 1 ? k / 2 : k, high = kM == 1 ? k % 2 : h / 8, g = kM == 1 ? h : h % 8;
           if constexpr (kBits == 8) {
@@ -311,12 +315,13 @@ struct Query {
         }
       }
 #pragma unroll
-      for (int k = 0; k < 3; ++k) sum[k] = __reduce_add_sync(0xffffffffu, sum[k]);
-      // the offset of the stored codes times a row's digits: of the first two digits together, and of the third
+      for (int k = 0; k < kDigits; ++k) sum[k] = __reduce_add_sync(0xffffffffu, sum[k]);
+      // the offset of the stored codes times a row's digits: of the first two digits together, and of the others.  The
+      // factor of the scores (as exponents of 2) is scale * 2^(e - 127 - 30) * log2(e), the power again in two factors.
       if (lane == 0) {
-        s_mul[h] = !key_finite(key) ? quiet_nan() : use ? scale * kLog2e * inverse(r) : 0.f;
-        s_dig[0][h] = -(1 << (kBits - 1)) * (256 * sum[0] + sum[1]);
-        s_dig[1][h] = -(1 << (kBits - 1)) * sum[2];
+        s_mul[h] = !key_finite(key) ? quiet_nan() : use ? scale * __int_as_float((e - 22) << 23) * (kLog2e / 256.f) : 0.f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) s_dig[k][h] = -(1 << (kBits - 1)) * (256 * sum[2 * k] + sum[2 * k + 1]);
       }
     }
   }
@@ -539,7 +544,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
     query.write(smem, s_dig, s_mul, heads, a.scale, warp, lane);
     __syncthreads();
     float mul[kM];
-    int32_t start[2][kM];  // the offset's part of the first two digits' sums together, and of the third's
+    int32_t start[2][kM];  // the offset's part of the first two digits' sums together, and of the others'
 #pragma unroll
     for (int r = 0; r < kM; ++r) {
       mul[r] = s_mul[g + 8 * r];
@@ -585,8 +590,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
             for (int j = 0; j < 2; ++j) {
               const uint32_t b0 = kBits == 8 ? w[j][kBits == 8 ? 2 * st : 0] : w[j][kBits == 8 ? 0 : st] & 0x0F0F0F0Fu;
               const uint32_t b1 = kBits == 8 ? w[j][kBits == 8 ? 2 * st + 1 : 0] : w[j][kBits == 8 ? 0 : st] >> 4 & 0x0F0F0F0Fu;
-              if (kM == 1 && op == 1) mma_s8u8(acc[j][op], q.x, 0u, q.z, 0u, b0, b1);  // rows 8-15 hold no digit
-              else mma_s8u8(acc[j][op], q.x, q.y, q.z, q.w, b0, b1);
+              mma_s8u8(acc[j][op], q.x, q.y, q.z, q.w, b0, b1);
             }
           }
         }
@@ -595,10 +599,12 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
 #pragma unroll
           for (int j = 0; j < kMine; ++j) {
             const auto& sum = acc[j >> 1];
-            const int32_t d0 = kM == 1 ? sum[0][j & 1] : sum[0][2 * r + (j & 1)];
-            const int32_t d1 = kM == 1 ? sum[0][2 + (j & 1)] : sum[kM - 1][2 * r + (j & 1)];
-            const int32_t d2 = kM == 1 ? sum[1][j & 1] : sum[kM][2 * r + (j & 1)];
-            x[r][j] = fmaf((float)(d0 * 256 + d1 + start[0][r]), 256.f, (float)(d2 + start[1][r]));
+            int32_t d[kDigits];
+#pragma unroll
+            for (int k = 0; k < kDigits; ++k)
+              d[k] = kM == 1 ? sum[k / 2][k % 2 * 2 + (j & 1)] : sum[kM == 1 ? 0 : k][2 * r + (j & 1)];
+            // at 256 dimensions 256 * d[0] + d[1] still lies within 2^31
+            x[r][j] = fmaf((float)(d[0] * 256 + d[1] + start[0][r]), 65536.f, (float)(d[2] * 256 + d[3] + start[1][r]));
           }
       }
       float ks[kMine], vs[kMine];

@@ -570,8 +570,9 @@ imq_status imq_paged_attention_workspace(const imq_kv_cache *cache, int64_t batc
  * 0 .. seq_lens[b] - 1 of sequence b, and the key head h / (n_q_heads / n_heads) of query head h:
  *   s_t = scale * sum_d Q[b, h, d] * key_t[d],  out[b, h, :] = sum_t softmax(s)_t * value_t,
  *   lse[b, h] = log sum_t exp(s_t)
- * Scores, softmax statistics and sums are fp32.  Codes enter the products exactly; a query entry as an integer
- * multiple of 2^-23 of its row's largest (a row below 1e-30 counts as zeros); a probability times its
+ * Scores, softmax statistics and sums are fp32.  Codes enter the products exactly; a query entry to 2^-30 of
+ * its row's largest, which keeps all bits of fp32 entries down to 2^-6 of it and of bf16 entries down to 2^-22 (a row
+ * below 1e-30 counts as zeros); a probability times its
  * value's step with 22 bits, or to 2^-36 of the largest such product of its query head where that is more (the step 1 of
  * a vector of zeros aside: it adds nothing and costs the others nothing).  The order of the sums is fixed: equal
  * inputs give equal bits.

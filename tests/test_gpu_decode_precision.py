@@ -112,3 +112,50 @@ def test_large_values_of_no_weight(imq, D, bits, G):  # noqa: F811
         k[at, :, 3], Q[..., 3] = -40.0, 1.5 * D ** 0.5
         cache, table, lens = filled(imq, k, v, bits)
         check(imq, cache, Q, table, lens)
+
+
+@pytest.mark.parametrize("heavy", [30.0, 1e3, 1e5, 2.0 ** 20])
+@pytest.mark.parametrize("D,bits,G", SHAPES)
+def test_heavy_query_dimensions(imq, D, bits, G, heavy):  # noqa: F811
+    """A query entry far above its row's others, on keys that are zero there.  The scores of the others are off by what fp32
+    sums cost and by 2^-30 of the largest entry; entries of few bits, down to 2^-22 of the largest, lose nothing.  One
+    token a sequence: its log sum is the score."""
+    H, n, page, at = 2, 40, 16, D - 5
+    K, V = _randn(1, n, H, D), _randn(2, n, H, D)
+    K[..., at] = 0
+    cache = imq.KVCache.zeros(n, page, H, D, bits)
+    imq.imq_kv_write(cache, K, V, torch.arange(n, device="cuda") * page)
+    table, lens = torch.arange(n, dtype=torch.int32, device="cuda")[:, None], torch.ones(n, dtype=torch.int32, device="cuda")
+    k = cache_values(cache)[0][::page].astype(np.float64)  # (n, H, D)
+    v = cache_values(cache)[1][::page]
+    whole = torch.randint(-8, 9, (n, H * G, D), generator=torch.Generator().manual_seed(3)).cuda()
+    for Q, grid in ((_randn(4, n, H * G, D), 2.0 ** -30), (_randn(5, n, H * G, D, dtype=torch.bfloat16), 2.0 ** -30),
+                    (whole.float(), 0.0), (whole.bfloat16(), 0.0)):
+        Q[..., at] = heavy
+        out, lse = imq.imq_paged_attention(cache, Q, table, lens, out_dtype=torch.float32)
+        q = f64(Q).reshape(n, H, G, D)
+        scale = D ** -0.5
+        x = scale * np.einsum("nhgd,nhd->nhg", q, k)
+        mass = np.einsum("nhgd,nhd->nhg", np.abs(q), np.abs(k))
+        tol = scale * ((D // 16 + 16) * U * mass + grid * np.abs(q).max(-1) * np.abs(k).sum(-1)[..., None]) + 8 * U * np.abs(x)
+        assert (np.abs(f64(lse).reshape(x.shape) - x) <= tol).all()
+        want = np.broadcast_to(v[:, :, None], q.shape)
+        assert (np.abs(f64(out).reshape(q.shape) - want) <= 2.0 ** -20 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("top", [1.0, 1.984375, 1.9999999, 1.9921875, 1.5])
+@pytest.mark.parametrize("exponent", [-99, -3, 0, 40, 127])
+def test_largest_query_entries(imq, top, exponent):  # noqa: F811
+    """Rows whose largest entries stand at the ends of what the first digit holds, both signs, over fp32's exponents."""
+    D, n = 128, 1
+    K = torch.full((n, 1, D), 127.0, device="cuda")  # codes of 127 and -127, a step of 1
+    K[..., ::2] = -127.0
+    cache, table, lens = filled(imq, K, K, 8, page=16)
+    Q = torch.zeros(1, 4, D, device="cuda")
+    big = float(np.float32(top) * np.float32(2.0) ** exponent)
+    Q[0, 0, 0], Q[0, 1, 1], Q[0, 2, ::2], Q[0, 3, 1::2] = big, -big, big, big
+    Q[0, 2, 6] = -big
+    scale = 2.0 ** -exponent / 128
+    _, lse = imq.imq_paged_attention(cache, Q, table, lens, scale=scale)
+    x = scale * f64(Q)[0] @ f64(K)[0, 0]
+    assert (np.abs(f64(lse)[0] - x) <= 8 * U * np.abs(x)).all()
