@@ -845,6 +845,8 @@ def imq_paged_attention(cache: KVCache, Q: torch.Tensor, block_table: torch.Tens
         if lse.dtype is not torch.float32 or lse.shape != (batch, heads) or (heads > 1 and lse.stride(1) != 1):
             raise ValueError("lse must be float32 (batch, query heads) with unit stride in the last axis")
         lse_ptr, lse_stride = lse.data_ptr(), lse.stride(0)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     dev = _device(cache.k, Q, block_table, seq_lens, out, lse, workspace)
     need = imq_paged_attention_workspace(cache, batch, heads, max_len)
     if workspace is not None:
