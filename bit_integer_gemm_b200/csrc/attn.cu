@@ -1015,6 +1015,7 @@ imq_status launch_paged_attention(const imq_kv_cache* c, const void* Q, imq_dtyp
       ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(lens) | reinterpret_cast<uintptr_t>(table)) & 3) ||
       (reinterpret_cast<uintptr_t>(workspace) & 15))
     return IMQ_ERR_ARG;
+  if (!vectors_apart(batch, o_batch, q_heads, o_head, c->head_dim) || (lse && batch > 1 && lse_batch < q_heads)) return IMQ_ERR_ARG;
   AttnArgs a = {};
   a.c = *c;
   a.k_stride16 = (uint32_t)(c->k_page_stride / 16), a.v_stride16 = (uint32_t)(c->v_page_stride / 16);

@@ -167,6 +167,9 @@ imq_status launch_w4_matvec(const uint8_t* codes, int64_t ldc, const float* step
                             int64_t ldy, cudaStream_t st);
 // The paged cache (kv.cu): imq_kv_*; check_cache is what every call on a cache checks first.
 imq_status check_cache(const imq_kv_cache* cache);
+// Whether no two of n x heads vectors of `dim` entries, vector (i, h) at i * step + h * head_step, share an entry: what
+// every call that writes such vectors checks.
+bool vectors_apart(int64_t n, int64_t step, int64_t heads, int64_t head_step, int64_t dim);
 imq_status launch_kv_write(const imq_kv_cache* c, const void* K, int64_t k_tok, int64_t k_head, const void* V, int64_t v_tok,
                            int64_t v_head, imq_dtype t, int64_t n, const int64_t* slots, cudaStream_t st);
 imq_status launch_kv_read(const imq_kv_cache* c, const int64_t* slots, int64_t n, void* K, int64_t k_tok, int64_t k_head,

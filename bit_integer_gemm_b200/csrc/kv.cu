@@ -288,6 +288,9 @@ imq_status launch(bool write, const imq_kv_cache* cache, void* K, int64_t k_tok,
   if (!slots || (write && (!K || !V)) || (!K && !V) || ((kp | vp) & (size - 1)) || (reinterpret_cast<uintptr_t>(slots) & 7))
     return IMQ_ERR_ARG;
   if (n > INT32_MAX / cache->n_heads) return IMQ_ERR_UNSUPPORTED;
+  if (!write && ((K && !vectors_apart(n, k_tok, cache->n_heads, k_head, cache->head_dim)) ||
+                 (V && !vectors_apart(n, v_tok, cache->n_heads, v_head, cache->head_dim))))
+    return IMQ_ERR_ARG;
   DeviceState* ds;
   s = device_state(&ds);
   if (s != IMQ_OK) return s;
@@ -306,6 +309,20 @@ imq_status launch(bool write, const imq_kv_cache* cache, void* K, int64_t k_tok,
   return cudaGetLastError() == cudaSuccess ? IMQ_OK : IMQ_ERR_CUDA;
 }
 }  // namespace
+
+bool vectors_apart(int64_t n, int64_t step, int64_t heads, int64_t head_step, int64_t dim) {
+  if (n <= 1 || heads <= 1) return (n <= 1 || step >= dim) && (heads <= 1 || head_step >= dim);
+  if (step < dim || head_step < dim) return false;
+  // one axis within the other's step: every layout of a tensor's axes
+  if ((step - dim) / head_step >= heads - 1 || (head_step - dim) / step >= n - 1) return true;
+  // else two vectors d heads apart are nearest where their tokens' distance is d * head_step, rounded either way
+  for (int64_t d = 1; d < heads; ++d) {
+    const int64_t from = head_step > INT64_MAX / d ? INT64_MAX : d * head_step, i = from / step, rest = from % step;
+    if (i < n && rest < dim) return false;
+    if (i + 1 < n && step - rest < dim) return false;
+  }
+  return true;
+}
 
 imq_status check_cache(const imq_kv_cache* c) {
   if (!c) return IMQ_ERR_ARG;

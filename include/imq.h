@@ -554,8 +554,8 @@ imq_status imq_kv_write(const imq_kv_cache *cache, const void *K, int64_t k_toke
 
 /*
  * imq_kv_read -- the values of n slots, rounded once to yt, into K and V (either may be NULL), addressed as
- * in imq_kv_write.  Slots may repeat.  The outputs of a negative slot are left as they were, those of a slot
- * outside the cache too, which sets IMQ_ERR_BOUNDS.
+ * in imq_kv_write; no two of an output's vectors may overlap (IMQ_ERR_ARG).  Slots may repeat.  The outputs of a
+ * negative slot are left as they were, those of a slot outside the cache too, which sets IMQ_ERR_BOUNDS.
  */
 imq_status imq_kv_read(const imq_kv_cache *cache, const int64_t *slots, int64_t n, void *K, int64_t k_token_stride,
                        int64_t k_head_stride, void *V, int64_t v_token_stride, int64_t v_head_stride, imq_dtype yt,
@@ -585,8 +585,9 @@ imq_status imq_paged_attention_workspace(const imq_kv_cache *cache, int64_t batc
  * max_len     no sequence is longer (at most table_width * page_size); it sizes the launch.  A longer sequence
  *             has out and lse NaN and sets IMQ_ERR_BOUNDS in the status word; so has one whose page lies outside
  *             the cache.
- * out         device, dtype ot (F32 or BF16), addressed as Q; must not overlap it.   lse: device fp32 or NULL, row b
- *             at b * lse_batch_stride.
+ * out         device, dtype ot (F32 or BF16), addressed as Q; must not overlap it, nor one of its vectors another
+ *             (IMQ_ERR_ARG).
+ * lse         device fp32 or NULL, row b at b * lse_batch_stride; rows must not overlap (IMQ_ERR_ARG).
  * workspace   device, 16-byte aligned, at least imq_paged_attention_workspace bytes (IMQ_ERR_BUFFER otherwise); need
  *             not be initialised.  Calls whose executions overlap, and graphs that replay at the same time,
  *             need workspaces of their own.
