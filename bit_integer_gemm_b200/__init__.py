@@ -790,7 +790,12 @@ def imq_kv_read(cache: KVCache, slots: torch.Tensor, dtype=torch.float32, K=None
 
 
 def imq_paged_attention_workspace(cache: KVCache, batch: int, n_q_heads: int, max_len: int) -> int:
-    """Workspace bytes of imq_paged_attention for these sizes."""
+    """Workspace bytes of imq_paged_attention for these sizes on the cache's device, which has to be the current one."""
+    _device(cache.k)
+    return _workspace_bytes(cache, batch, n_q_heads, max_len)
+
+
+def _workspace_bytes(cache: KVCache, batch: int, n_q_heads: int, max_len: int) -> int:
     key = (batch, n_q_heads, max_len)
     need = cache._workspace.get(key)
     if need is None:
@@ -848,7 +853,7 @@ def imq_paged_attention(cache: KVCache, Q: torch.Tensor, block_table: torch.Tens
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     dev = _device(cache.k, Q, block_table, seq_lens, out, lse, workspace)
-    need = imq_paged_attention_workspace(cache, batch, heads, max_len)
+    need = _workspace_bytes(cache, batch, heads, max_len)
     if workspace is not None:
         room, room_ptr = workspace.numel() * workspace.element_size(), workspace.data_ptr()
     elif need:

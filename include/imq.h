@@ -561,7 +561,8 @@ imq_status imq_kv_read(const imq_kv_cache *cache, const int64_t *slots, int64_t 
                        int64_t k_head_stride, void *V, int64_t v_token_stride, int64_t v_head_stride, imq_dtype yt,
                        imq_stream_t stream);
 
-/* imq_paged_attention_workspace -- device bytes imq_paged_attention needs for these sizes (may be 0). */
+/* imq_paged_attention_workspace -- device bytes imq_paged_attention needs for these sizes on the current device
+ * (may be 0). */
 imq_status imq_paged_attention_workspace(const imq_kv_cache *cache, int64_t batch, int32_t n_q_heads, int64_t max_len,
                                          size_t *bytes);
 

@@ -66,3 +66,12 @@ def test_log_sums_that_overlap_are_refused(lib):
     for rows in (0, 1):
         assert lib.imq_paged_attention(ctypes.addressof(c), P, imq.IMQ_BF16, 0, 0, 2, 2, P, 4, 4, P, 64, 1.0, P, imq.IMQ_BF16, 128, 64, P,
                                        rows, P, 1 << 30, None) == imq.IMQ_ERR_ARG
+
+
+def test_workspace_sizes_are_the_current_devices():
+    """They count the device's SMs, and the binding keeps them with the cache: asked of another device, they would be
+    another's."""
+    c = imq.KVCache.zeros(3, 16, 2, 64, 8, device="cpu")
+    with pytest.raises(ValueError, match="current CUDA device"):
+        imq.imq_paged_attention_workspace(c, 1, 2, 48)
+    assert not c._workspace
