@@ -510,8 +510,10 @@ imq_status imq_w4_dequantize(const uint8_t *codes, int64_t ldc, const float *ste
  *   Y[m, n] = sum over groups g of steps[n, g] * sum_{k in g} code[n, k] * X[m, k]
  * with exact products and fp32 sums, rounded once to yt.  The weight is read once per 16 tokens; for many
  * tokens use the GEMM above.  The order of the sums is fixed: equal inputs give equal bits.
- * X       device, M x K, dtype xt (F32 or BF16), leading dimension ldx (>= K).  fp32 entries keep all their
- *         bits.  A non-finite entry gives its token non-finite outputs.
+ * X       device, M x K, dtype xt (F32 or BF16), leading dimension ldx (>= K).  fp32 entries of 2^-109 and more
+ *         keep all their bits, smaller ones those above 2^-133.  A group's sum of code * X is formed before its step
+ *         is applied: entries above 2^118 may make it, and the token's outputs, infinite.  A non-finite entry gives
+ *         its token non-finite outputs.
  * Y       device, M x N, dtype yt (F32 or BF16), leading dimension ldy (>= N).  K = 0 gives zeros.  Must not
  *         overlap X.
  * Errors: IMQ_ERR_ARG; IMQ_ERR_UNSUPPORTED for M above 1 048 560.

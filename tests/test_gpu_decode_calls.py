@@ -24,3 +24,17 @@ def test_outputs_laid_out_by_heads(imq):  # noqa: F811
     with pytest.raises(imq.ImqError) as e:
         imq.imq_paged_attention(cache, Q, table, n, out=torch.zeros(len(lens), 1, D, device="cuda").expand(-1, H * G, -1))
     assert e.value.status == imq.IMQ_ERR_ARG
+
+
+@pytest.mark.parametrize("exponent", [-109, -100, 0, 100, 117])
+def test_ends_of_a_products_range(imq, exponent):  # noqa: F811
+    """fp32 entries from 2^-109 to 2^118 keep all their bits: their last part lies above bf16's smallest spacing, and a
+    group's sum, up to 128 entries times codes of 7, within fp32.  One weight of step 1 and code 7 and its product, then
+    groups whose sum has one sign.  (An exact product passes the sums of three parts; one of 128 of them, its inner steps, too.)"""
+    x = (1 + torch.rand(9, 1, generator=torch.Generator().manual_seed(exponent), dtype=torch.float64)).float().cuda() * 2.0 ** exponent
+    one = imq.imq_w4_quantize(torch.full((1, 5), 7.0, device="cuda"), 32)
+    y = imq.imq_w4_matvec(one, x).double()
+    assert ((y - 7 * x.double()).abs() <= 3 * 2.0 ** -23 * y).all()
+    many = imq.imq_w4_quantize(torch.full((128, 5), 7.0, device="cuda"), 128)
+    y = imq.imq_w4_matvec(many, x.expand(9, 128).contiguous()).double()
+    assert ((y - 896 * x.double()).abs() <= 40 * 2.0 ** -23 * y).all()
