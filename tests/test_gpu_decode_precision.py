@@ -159,3 +159,17 @@ def test_largest_query_entries(imq, top, exponent):  # noqa: F811
     _, lse = imq.imq_paged_attention(cache, Q, table, lens, scale=scale)
     x = scale * f64(Q)[0] @ f64(K)[0, 0]
     assert (np.abs(f64(lse)[0] - x) <= 8 * U * np.abs(x)).all()
+
+
+@pytest.mark.parametrize("D,bits,G", SHAPES)
+def test_values_that_grow_from_nothing(imq, D, bits, G):  # noqa: F811
+    """Whole runs of zeros and of 1e-30, then values of 1, 1e4 and 1e30, with equal and with unequal weights."""
+    H, n = 2, 320
+    K, V, Q = _randn(1, n, H, D), _randn(2, n, H, D), _randn(3, 1, H * G, D)
+    size = torch.zeros(n, device="cuda")
+    size[64:128], size[128:192], size[192:256], size[256:] = 1e-30, 1.0, 1e4, 1e30
+    for at in (64, 128, 192, 256, 320):
+        cache, table, lens = filled(imq, K, V * size[:, None, None], bits)
+        lens[0] = at
+        check(imq, cache, Q, table, lens)
+        check(imq, cache, Q, table, lens, scale=0.0)
