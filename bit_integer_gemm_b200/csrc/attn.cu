@@ -32,17 +32,19 @@
 // Split: the work of all sequences and key heads lies in one line of units of 64 tokens, cut into equal parts, one
 // for each CTA that the SMs hold at once; so lengths may differ as they will.  A row (one sequence's tokens of one key
 // head) counts four units more than it has, for its queries and its end: without them a CTA whose part is made of many
-// short rows came last (64 sequences of 1 to 4097 tokens, 8 key heads of 64: 47.2 us, with them 32.6; 16 of up to 8192
-// at 4 bits: 37.0 and 29.0; 2 or 6 to 12 instead of four: 32.6 to 36.2 and 29.4 to 31.0).  A CTA's four warps take runs
-// of 16 tokens in turn, each with its own ring of asynchronous copies (so that a run waits for no barrier but the
-// warp's), and join in shared memory.  Rows that several CTAs share join in k_attn_join from partial sums in the
-// workspace, in a fixed order.
+// short rows came last (64 sequences of 1 to 4097 tokens, 8 key heads of 64: 50.1 us, with them 34.6; 16 of up to 8192
+// at 4 bits: 38.8 and 29.7; 64 of up to 2048, 4 key heads of 256: 44.5 and 30.9; 256 of up to 600: 76 and 52.  Of
+// thirteen such mixes one takes 25 % more with 2 units, 7 % with 6, 13 % with 8, and one, of 16 heads a key head, 6 % less
+// with 6).  A CTA's four warps take runs of 16 tokens in turn, each with its own ring of asynchronous copies (so that a run waits for
+// no barrier but the warp's), and join in shared memory.  Rows that several CTAs share join in k_attn_join from partial
+// sums in the workspace, in a fixed order.
 //
-// Measured, both kernels: 64 sequences of 2048 tokens, 32 key heads of 128 at 8 bits, 178 us (6.2 TB/s); one of 131072, 8
+// Measured, both kernels: 64 sequences of 2048 tokens, 32 key heads of 128 at 8 bits, 175 us (6.3 TB/s); one of 131072, 8
 // heads, 52 us (5.3 TB/s: memory, and about 8 us of start, ends and join); 64 of 8192 at 4 bits 154 us (3.7 TB/s: a code
-// takes as many instructions as at 8 bits, 345 for 16 tokens and 128 entries, and half the bytes); head size 64 at 8
-// query heads a key head 57 us for 64 of 4096 (5.0 TB/s), size 256 99 us for 64 of 2048 (5.5 TB/s); one sequence of 2048
-// tokens and 32 heads 10.1 us, which is two dependent launches and a CTA's chain of dependent loads.
+// takes as many instructions as at 8 bits, 337 to 356 for 16 tokens and 128 entries, and half the bytes); head size 64
+// at 8 query heads a key head 57 us for 64 of 4096 (5.0 TB/s), size 256 94 us for 64 of 2048 (5.8 TB/s); 16 query heads a
+// key head, 64 of 4096, 4 key heads of 128: 80 us (3.5 TB/s; twice the matrix instructions, spills); one sequence of 2048
+// tokens and 32 heads 10.0 us, which is two dependent launches and a CTA's chain of dependent loads.
 #include <atomic>
 #include <type_traits>
 
@@ -231,7 +233,7 @@ struct Shape {
   static constexpr int kStages = 13000 / kRunBytes < 2 ? 2 : 13000 / kRunBytes > 8 ? 8 : 13000 / kRunBytes;
   static constexpr int kRing = kStages * kRunBytes;
   // CTAs an SM, by the registers of the sums.  At 128 a fourth would cost spills: three take 52 us for 131072 tokens of
-  // 8 key heads at 8 bits, four 55.
+  // 8 key heads at 8 bits, four 73.
   static constexpr int kPerSm = kD <= 64 ? 4 : kD <= 128 ? 3 : 2;
   static constexpr int kHeads = 8 * kM;
   static constexpr int kQOps = kDigits / 2 * kM;       // operands of the digits, 512 bytes each a step
@@ -795,9 +797,9 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kBits, kD, kM>::kPerSm) k_a
 constexpr int kJoinWarps = 8;
 
 // Joins the parts of a row that several CTAs hold.  A lane has four entries (and four more at 128).  Few parts: a warp
-// takes a head; many: all warps share a head's parts (always: 41.6 us for 64 sequences of 1 to 4097 tokens, 32.6 as it
-// is).  A CTA takes a row; a head where that makes no more CTAs than two to one of k_attn's (one sequence of 131072: 52.6
-// us, by rows 58.9; the 64 sequences by heads: 45.2 us).
+// takes a head; many: all warps share a head's parts (always: 43.5 us for 64 sequences of 1 to 4097 tokens, 34.6 as it
+// is).  A CTA takes a row; a head where that makes no more CTAs than two to one of k_attn's (one sequence of 131072: 51.7
+// us, by rows 58.0; the 64 sequences by heads: 47.1 us).
 __global__ void __launch_bounds__(kJoinWarps * 32, 4) k_attn_join(const __grid_constant__ AttnArgs a, int heads_of_cta, int per_head) {
   __shared__ float s_num[kJoinWarps][256], s_den[kJoinWarps], s_top[kJoinWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.y;

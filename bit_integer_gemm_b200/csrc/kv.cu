@@ -4,9 +4,9 @@
 // A vector (one head's key or value of one token) is one quantisation group.  D / 8 lanes take a vector, 8
 // entries each: the largest |x| by shuffles, the codes packed to one word (4 bits) or two (8 bits) a lane.
 // A lane group does a token's key and value of a head together, so their two steps are one 8-byte store.
-// Bound: memory; every entry is read and written once.  Reading back runs at 5.8 TB/s (65536 tokens of 8 heads of 128, 8
-// bits to bf16).  Writing has the instructions of the quantiser besides, seven an entry, and reaches 4.1 (of the reads of
-// one tensor and all writes, 66.6 us); 8191 tokens at 4 bits take 9.9 us.
+// Bound: memory; every entry is read and written once.  65536 tokens of 8 heads of 128, bf16 and 8 bits: written in 69.0 us
+// (5.9 TB/s, keys and values two tensors), read back in 64.9 (6.3 TB/s).  Writing has the instructions of the quantiser
+// besides, seven an entry: 8191 tokens at 4 bits take 12.4 us (3.4 TB/s), issue slots 62 % busy in 42 % of the warps.
 #include <type_traits>
 
 #include "lowbit.cuh"
@@ -31,8 +31,8 @@ struct VecArgs {
 };
 
 // Tokens a lane group takes, their loads under way together: four where that still fills the SMs twice (65536 tokens of
-// 8 heads at 8 bits: 66.6 us written and 69.8 read; with one 76.8 and 82.0), one below (32 tokens of 32 heads written and
-// 64 read: 3.9 us; with four 5.9).
+// 8 heads at 8 bits: 69.0 us written and 64.9 read; with one 79.8 and 75.9), one below (32 tokens of 32 heads: 2.0 us
+// written, 1.8 read; with four 3.3 and 2.7).
 constexpr int kManyTokens = 4;
 
 // Where a token's vectors of a head lie: in the keys and the values, and their page in the steps, in 16 bytes (every
@@ -121,7 +121,7 @@ __device__ __forceinline__ void store_vec(float* p, const float (&x)[4]) {
 }
 
 // kLanes: lanes of a vector's group (a power of two >= D / 8; the lanes at and above D / 8 hold zeros).
-// bf16: four CTAs an SM, at the price of a few spilled registers (66.6 us for the 65536 tokens; three without: 70.6).
+// bf16: four CTAs an SM, at the price of a few spilled registers (69.0 us for the 65536 tokens; three without: 72.9).
 template <typename T, int kBits, int kLanes, int kTokens>
 __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) k_kv_write(const __grid_constant__ VecArgs a) {
   const imq_kv_cache& c = a.c;

@@ -162,11 +162,12 @@ __device__ __forceinline__ uint32_t nibbles_f16(uint32_t w, uint32_t one) {
   if (kHigh) return h2_fma(and_or(w, 0x00F000F0u, one), 0x2C002C00u /* 1/16 */, 0xD480D480u /* -72 */);
   return h2_sub(and_or(w, 0x000F000Fu, one), 0x64086408u /* 1032 */);
 }
-// fp16 pair of the 8-bit codes in the bytes of x that `sel` names (0-3), as __byte_perm selectors 0x4y4x.
+// fp16 pair of the 8-bit codes in the bytes of x that `sel` names (0-3), as a __byte_perm selector 0x5y5x (5: the high byte of
+// `one`).
 __device__ __forceinline__ uint32_t bytes_f16(uint32_t x, uint32_t sel, uint32_t one) {
   return h2_sub(__byte_perm(x, one, sel), 0x64806480u /* 1152 */);
 }
-// Codes 2i and 2i + 1 of a word of eight 4-bit codes, and bytes i and i + 1 of a word, as fp32.
+// Codes 2i and 2i + 1 of a word of eight 4-bit codes, and bytes 2i and 2i + 1 of a word, as fp32.
 __device__ __forceinline__ float2 nibble_pair(uint32_t w, int i, uint32_t one) {
   const uint32_t h = i == 0   ? nibbles_f16<false>(w, one)
                      : i == 1 ? nibbles_f16<true>(w, one)

@@ -322,11 +322,13 @@ __global__ void __launch_bounds__(128) k_w4_dequantize_cols(DequantArgs a) {
 // ------------------------------------------------------------------------------------------------
 // Y = X * W for a few tokens
 // ------------------------------------------------------------------------------------------------
-// The weight is read once, N K / 2 bytes and the steps, for 2 M N K operations.  What bounds it is not that memory but
-// turning codes into operands, eleven instructions for eight codes (seven of them integer).  So the product runs on
+// The weight is read once per 16 tokens, N K / 2 bytes and the steps, for 2 M N K operations.  Memory does not bound it:
+// turning codes into operands takes eleven instructions for eight codes (seven of them integer).  So the product runs on
 // the warp-level tensor core instruction with the weight as the 16-row operand: a conversion serves 8 tokens at once.
-// One bf16 token: 4096 x 4096 in 4.3 us, 11008 x 4096 in 8.6 (2.9 TB/s); 8 tokens, 4096 x 22016: 16.0 us (3.0 TB/s), the
-// SMs issuing in 58 % of their cycles; 3 fp32 tokens, 4099 x 11007: 20.2 us.
+// No unit is full either (issue slots 37 to 58 %, integer pipe 34 to 52 %, 12 to 24 % of the warps): the warps are few and
+// wait on their own chains, and sets of channels come in whole rounds (688 sets on 296 CTAs: three rounds for 2.3).
+// One bf16 token: 4096 x 4096 in 4.3 us, 11008 x 4096 in 8.6 (2.9 TB/s); 8 tokens, 4096 x 22016: 16.0 us (3.0 TB/s), 16: 22.8,
+// 24: 42; 3 fp32 tokens, 4099 x 11007: 20.1 us.
 //   - Codes in -7 .. 7 are exact in bf16, and bf16 entries of X are operands as they are.
 //   - An fp32 entry is cut into three bf16 parts of 8 bits, exact together: a column of the other operand for each
 //     part with up to 2 tokens, an operand for each part with more.
